@@ -346,6 +346,7 @@ int nabla_status(const void *workspace, nabla_stream_t stream) {
     int word = 0;
     if (cudaMemcpy(&word, workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
         return NABLA_ERR_CUDA;
+    if (word == nabla::kDevParam) return NABLA_ERR_PARAM;
     return word == nabla::kDevOk ? NABLA_OK : NABLA_ERR_TIMEOUT;
 }
 

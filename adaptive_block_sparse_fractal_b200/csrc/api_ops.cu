@@ -1,0 +1,470 @@
+// C ABI of the calls around the grid attention (declared in include/nabla.h):
+// rotary positions, packed-sequence attention, the paged key-value cache.
+// Argument checks, workspace layout, kernel dispatch; every host-detectable
+// error is returned before anything is enqueued.
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/nabla.h"
+#include "packed.cuh"
+#include "paged.cuh"
+#include "rope.cuh"
+
+// launchers (rope.cu, packed_fwd.cu, paged.cu)
+cudaError_t nabla_launch_rope(nabla::RopeArgs &a, int dtype, int layout, int wide,
+                              cudaStream_t stream);
+cudaError_t nabla_launch_packed_fwd(const nabla::packed::Args &a, int D, int64_t units, int splits,
+                                    cudaStream_t stream);
+cudaError_t nabla_launch_append(const nabla::AppendArgs &a, cudaStream_t stream);
+cudaError_t nabla_launch_paged(const nabla::PagedArgs &a, cudaStream_t stream);
+
+namespace {
+
+constexpr size_t kStatusBytes = 256;
+constexpr int64_t kMaxExtent = 1ll << 46;  // bytes a view may span: keeps the arithmetic in 64 bits
+
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? NABLA_OK : NABLA_ERR_CUDA; }
+cudaStream_t as_stream(nabla_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+int check_workspace(const void *ws, size_t bytes, size_t need) {
+    if (ws == nullptr || bytes < need) return NABLA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return NABLA_ERR_ALIGN;
+    return NABLA_OK;
+}
+
+// A view over [batch, heads, tokens, D] elements of `size` bytes.
+struct Box {
+    const nabla_view *v;
+    int64_t n[3], stride[3];  // batch, head, token: extents and distances (0 where the extent is 1)
+    int64_t D, size;
+    uintptr_t lo, hi;         // bytes it spans: [lo, hi)
+};
+
+// Extents and span; false for negative distances or a span beyond kMaxExtent.
+bool make_box(const nabla_view *v, int64_t B, int64_t heads, int64_t tokens, int64_t D, int size,
+              Box *b) {
+    b->v = v;
+    const int64_t n[3] = {B, heads, tokens}, s[3] = {v->batch, v->head, v->token};
+    int64_t last = D;
+    for (int i = 0; i < 3; ++i) {
+        b->n[i] = n[i];
+        b->stride[i] = n[i] > 1 ? s[i] : 0;
+        if (b->stride[i] < 0 || b->stride[i] > kMaxExtent) return false;
+        if (n[i] > 1 && b->stride[i] > kMaxExtent / n[i]) return false;
+        last += (n[i] - 1) * b->stride[i];
+    }
+    if (last > kMaxExtent / size) return false;
+    b->D = D;
+    b->size = size;
+    b->lo = reinterpret_cast<uintptr_t>(v->data);
+    b->hi = b->lo + static_cast<uintptr_t>(last) * size;
+    return true;
+}
+
+bool multiple_of_16(const Box &b) {
+    if ((b.lo & 15u) != 0) return false;
+    for (int i = 0; i < 3; ++i)
+        if (b.stride[i] * b.size % 16 != 0) return false;
+    return true;
+}
+
+// No two rows of a view that is written may share elements: walking its
+// dimensions from the closest together, each distance clears what lies inside.
+bool self_disjoint(const Box &b) {
+    bool used[3] = {b.n[0] == 1, b.n[1] == 1, b.n[2] == 1};
+    int64_t inner = b.D;
+    for (int round = 0; round < 3; ++round) {
+        int best = -1;
+        for (int i = 0; i < 3; ++i)
+            if (!used[i] && (best < 0 || b.stride[i] < b.stride[best])) best = i;
+        if (best < 0) break;
+        if (b.stride[best] < inner) return false;
+        inner += (b.n[best] - 1) * b.stride[best];
+        used[best] = true;
+    }
+    return true;
+}
+
+// Whether two views share no element: disjoint spans, or slices of one buffer
+// that repeat at the same token distance and lie beside each other in it.
+bool disjoint(const Box &a, const Box &b) {
+    if (a.hi <= b.lo || b.hi <= a.lo) return true;
+    const int64_t step = a.stride[2] * a.size;
+    if (step <= 0 || step != b.stride[2] * b.size) return false;
+    for (const Box *x : {&a, &b})
+        if (x->n[0] > 1 && x->stride[0] * x->size % step != 0) return false;
+    const int64_t wa = ((a.n[1] - 1) * a.stride[1] + a.D) * a.size;
+    const int64_t wb = ((b.n[1] - 1) * b.stride[1] + b.D) * b.size;
+    const int64_t d = b.lo >= a.lo ? static_cast<int64_t>((b.lo - a.lo) % step)
+                                   : (step - static_cast<int64_t>((a.lo - b.lo) % step)) % step;
+    return d >= wa && d + wb <= step;
+}
+
+bool same_view(const Box &a, const Box &b) {
+    return a.lo == b.lo && a.stride[0] == b.stride[0] && a.stride[1] == b.stride[1] &&
+           a.stride[2] == b.stride[2];
+}
+
+// ---------------------------------------------------------------------------
+// packed attention
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxPackedRows = (1ll << 31) - 1024;
+
+bool packed_shape_ok(const nabla_packed *s) {
+    return s->seqs >= 1 && s->heads >= 1 && s->heads_kv >= 1 && s->heads % s->heads_kv == 0 &&
+           (s->D == 64 || s->D == 128) && s->total_q >= 0 && s->total_k >= 0 &&
+           s->total_k <= kMaxPackedRows && s->total_q <= kMaxPackedRows / s->heads &&
+           s->seqs <= (1 << 24);
+}
+
+// 256-row forward units of all key heads, at most (every sequence may end inside one)
+int64_t fwd_units(const nabla_packed *s) {
+    const int64_t G = s->heads / s->heads_kv;
+    return (s->total_q * G / 256 + s->seqs) * s->heads_kv;
+}
+
+// Splits of the key range.  One CTA walks 128 keys in about a microsecond, so
+// few units against many keys leave SMs idle for long; at least 512 keys a
+// split (on average over the sequences) keep the join small against it.
+int fwd_splits(const nabla_packed *s) {
+    const int64_t units = fwd_units(s);
+    int64_t splits = 148 / units;
+    const int64_t most = s->total_k / s->seqs / 512;
+    if (splits > most) splits = most;
+    if (splits > 32) splits = 32;
+    return splits < 1 ? 1 : static_cast<int>(splits);
+}
+
+size_t packed_ws(const nabla_packed *s, int op) {
+    const int splits = fwd_splits(s);
+    size_t n = 0;
+    if (splits > 1)
+        n = round256(sizeof(float) * splits * s->total_q * s->heads * (s->D + 2));
+    if (op == NABLA_PACKED_BWD) {
+        const size_t pad = static_cast<size_t>((s->total_q / 64 + s->seqs) * 64);
+        const size_t b = 2 * round256(sizeof(float) * pad * s->heads);
+        if (b > n) n = b;
+    }
+    return kStatusBytes + n;
+}
+
+nabla::packed::View dev_view(const nabla_view *v) {
+    return {static_cast<__nv_bfloat16 *>(v->data), v->token, v->head};
+}
+
+int packed_view(const nabla_view *v, int64_t tokens, int heads, int D, bool written, Box *b) {
+    if (v == nullptr) return NABLA_ERR_NULL;
+    if (tokens == 0) return make_box(v, 1, 1, 1, D, 2, b) ? NABLA_OK : NABLA_ERR_PARAM;
+    if (v->data == nullptr) return NABLA_ERR_NULL;
+    if (!make_box(v, 1, heads, tokens, D, 2, b)) return NABLA_ERR_PARAM;
+    if (!multiple_of_16(*b)) return NABLA_ERR_ALIGN;
+    // the tensor maps of k, v, q, dout want distances above 0
+    for (int i = 1; i < 3; ++i)
+        if (b->n[i] > 1 && (b->stride[i] < 1 || b->stride[i] * 2 >= (1ll << 40)))
+            return NABLA_ERR_PARAM;
+    if (written && !self_disjoint(*b)) return NABLA_ERR_PARAM;
+    return NABLA_OK;
+}
+
+int check_packed(const nabla_packed *s, const int32_t *cu_q, const int32_t *cu_k, int op, void *ws,
+                 size_t bytes) {
+    if (s == nullptr) return NABLA_ERR_NULL;
+    if (!packed_shape_ok(s)) return NABLA_ERR_SHAPE;
+    if (!(s->scale > 0.f) || !std::isfinite(s->scale) || (s->causal != 0 && s->causal != 1))
+        return NABLA_ERR_PARAM;
+    if (cu_q == nullptr || cu_k == nullptr) return NABLA_ERR_NULL;
+    if (((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) & 3u) != 0)
+        return NABLA_ERR_ALIGN;
+    return check_workspace(ws, bytes, packed_ws(s, op));
+}
+
+nabla::packed::Args packed_args(const nabla_packed *s, const int32_t *cu_q, const int32_t *cu_k,
+                                void *ws) {
+    nabla::packed::Args a = {};
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.status = static_cast<int *>(ws);
+    a.total_q = s->total_q;
+    a.total_k = s->total_k;
+    a.seqs = s->seqs;
+    a.heads = s->heads;
+    a.heads_kv = s->heads_kv;
+    a.group = s->heads / s->heads_kv;
+    a.causal = s->causal;
+    a.c = s->scale * 1.4426950408889634f;
+    a.scale = s->scale;
+    a.limit = 1000000000u;  // 1 s per wait
+    return a;
+}
+
+// ---------------------------------------------------------------------------
+// paged cache
+// ---------------------------------------------------------------------------
+bool cache_shape_ok(const nabla_cache *c) {
+    return c->pages >= 1 && c->page_size >= 1 && c->heads_kv >= 1 && c->D >= 8 && c->D % 8 == 0 &&
+           c->D <= 256 && c->seqs >= 0 && c->table_width >= 1 && c->heads_kv <= (1 << 20);
+}
+
+int check_cache(const nabla_cache *c, bool written, Box bx[2], nabla::CacheArgs *a) {
+    if (c->k.data == nullptr || c->v.data == nullptr || c->table == nullptr) return NABLA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(c->table) & 3u) != 0) return NABLA_ERR_ALIGN;
+    const nabla_view *v[2] = {&c->k, &c->v};
+    for (int i = 0; i < 2; ++i) {
+        if (!make_box(v[i], c->pages, c->heads_kv, c->page_size, c->D, 2, &bx[i]))
+            return NABLA_ERR_PARAM;
+        if (!multiple_of_16(bx[i])) return NABLA_ERR_ALIGN;
+        if (written && !self_disjoint(bx[i])) return NABLA_ERR_PARAM;
+    }
+    a->k = static_cast<__nv_bfloat16 *>(c->k.data);
+    a->v = static_cast<__nv_bfloat16 *>(c->v.data);
+    a->k_page = bx[0].stride[0];
+    a->k_head = bx[0].stride[1];
+    a->k_token = bx[0].stride[2];
+    a->v_page = bx[1].stride[0];
+    a->v_head = bx[1].stride[1];
+    a->v_token = bx[1].stride[2];
+    a->table = c->table;
+    a->pages = c->pages;
+    a->page_size = c->page_size;
+    a->heads_kv = c->heads_kv;
+    a->D = c->D;
+    a->seqs = c->seqs;
+    a->width = c->table_width;
+    return NABLA_OK;
+}
+
+size_t paged_ws(const nabla_cache *c) {
+    return kStatusBytes + round256(sizeof(int) * nabla::kPagedCtas) +
+           sizeof(float) * 2 * nabla::kPagedCtas * nabla::kPagedHeads * (c->D + 2);
+}
+
+}  // namespace
+
+extern "C" {
+
+int nabla_rope(const nabla_rope_params *p, int B, int T, int H, int W, int P, int count,
+               const int *heads, const nabla_view *in, const nabla_view *out, const int32_t *pos,
+               int64_t pos_batch, int pos_axes, nabla_stream_t stream) {
+    if (p == nullptr || heads == nullptr || in == nullptr || out == nullptr) return NABLA_ERR_NULL;
+    if (B < 0 || T < 0 || H < 0 || W < 0 || count < 1 || count > 2) return NABLA_ERR_SHAPE;
+    if (p->dtype < NABLA_BF16 || p->dtype > NABLA_FP32 ||
+        (p->layout != NABLA_ROPE_ADJACENT && p->layout != NABLA_ROPE_HALVES) ||
+        (p->flags & ~(NABLA_ROPE_INVERSE | NABLA_ROPE_FLAT_IN | NABLA_ROPE_FLAT_OUT)) != 0)
+        return NABLA_ERR_PARAM;
+    if (p->D < 2 || p->D > 2 * nabla::kRopeMaxPairs || p->D % 2 != 0) return NABLA_ERR_SHAPE;
+    int R = 0;
+    for (int a = 0; a < 3; ++a) {
+        if (p->pairs[a] < 0 || p->pairs[a] > nabla::kRopeMaxPairs) return NABLA_ERR_PARAM;
+        R += p->pairs[a];
+        if (p->pairs[a] > 0 && (!(p->theta[a] > 0.0) || !std::isfinite(p->theta[a]) ||
+                                !std::isfinite(p->scale[a]) || !std::isfinite(p->offset[a])))
+            return NABLA_ERR_PARAM;
+        if (p->pairs[a] > 0 && pos != nullptr && a >= pos_axes) return NABLA_ERR_PARAM;
+    }
+    if (R < 1 || 2 * R > p->D) return NABLA_ERR_PARAM;
+    const bool flat = (p->flags & (NABLA_ROPE_FLAT_IN | NABLA_ROPE_FLAT_OUT)) != 0;
+    if (flat && (P < 1 || H % P != 0 || W % P != 0)) return NABLA_ERR_SHAPE;
+    if (pos != nullptr && (pos_axes < 1 || pos_axes > 3 || pos_batch < 0)) return NABLA_ERR_PARAM;
+    for (int i = 0; i < count; ++i)
+        if (heads[i] < 0 || heads[i] > (1 << 20)) return NABLA_ERR_SHAPE;
+    if (B == 0 || T == 0 || H == 0 || W == 0) return NABLA_OK;  // empty
+    const int64_t N = static_cast<int64_t>(T) * H <= INT32_MAX / W ? static_cast<int64_t>(T) * H * W : -1;
+    if (N < 0 || N > INT32_MAX - 256 || B > 65535) return NABLA_ERR_SHAPE;
+    const int size = p->dtype == NABLA_FP32 ? 4 : 2;
+    const int vec = 16 / size;
+    bool wide = p->D % vec == 0 && (p->layout == NABLA_ROPE_ADJACENT || R % vec == 0);
+    Box bi[2], bo[2];
+    int n = 0;
+    nabla::RopeArgs a = {};
+    for (int i = 0; i < count; ++i) {
+        if (heads[i] == 0) continue;  // nothing of this tensor
+        if (in[i].data == nullptr || out[i].data == nullptr) return NABLA_ERR_NULL;
+        if (!make_box(&in[i], B, heads[i], N, p->D, size, &bi[n]) ||
+            !make_box(&out[i], B, heads[i], N, p->D, size, &bo[n]))
+            return NABLA_ERR_PARAM;
+        if (bi[n].lo % size != 0 || bo[n].lo % size != 0) return NABLA_ERR_ALIGN;
+        wide = wide && multiple_of_16(bi[n]) && multiple_of_16(bo[n]);
+        if (!self_disjoint(bo[n])) return NABLA_ERR_PARAM;
+        a.t[n].in = in[i].data;
+        a.t[n].out = out[i].data;
+        a.t[n].in_batch = bi[n].stride[0];
+        a.t[n].in_head = bi[n].stride[1];
+        a.t[n].in_token = bi[n].stride[2];
+        a.t[n].out_batch = bo[n].stride[0];
+        a.t[n].out_head = bo[n].stride[1];
+        a.t[n].out_token = bo[n].stride[2];
+        a.t[n].heads = heads[i];
+        ++n;
+    }
+    if (n == 0) return NABLA_OK;
+    // in place: each thread writes exactly the elements it has read, if both
+    // sides have the same order (both flattened counts as the same)
+    const bool same_order = ((p->flags & NABLA_ROPE_FLAT_IN) != 0) == ((p->flags & NABLA_ROPE_FLAT_OUT) != 0);
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < n; ++j) {
+            if (!(i == j && same_order && same_view(bo[i], bi[i])) && !disjoint(bo[i], bi[j]))
+                return NABLA_ERR_PARAM;
+            if (i < j && !disjoint(bo[i], bo[j])) return NABLA_ERR_PARAM;
+        }
+    a.count = n;
+    a.B = B;
+    a.N = static_cast<int>(N);
+    a.T = T;
+    a.H = H;
+    a.W = W;
+    a.P = flat ? P : 1;
+    a.D = p->D;
+    a.pairs = R;
+    a.flat_in = (p->flags & NABLA_ROPE_FLAT_IN) != 0;
+    a.flat_out = (p->flags & NABLA_ROPE_FLAT_OUT) != 0;
+    a.pos = pos;
+    a.pos_batch = pos_batch;
+    a.pos_axes = pos_axes;
+    constexpr double kTwoPi = 6.283185307179586476925286766559;
+    for (int ax = 0, at = 0; ax < 3; ++ax) {
+        a.offset[ax] = p->pairs[ax] > 0 ? p->offset[ax] : 0.0;
+        for (int i = 0; i < p->pairs[ax]; ++i, ++at) {
+            const double f = std::pow(p->theta[ax], -static_cast<double>(i) / p->pairs[ax]);
+            a.axis[at] = static_cast<int8_t>(ax);
+            a.turn[at] = ((p->flags & NABLA_ROPE_INVERSE) ? -1.0 : 1.0) * p->scale[ax] * f / kTwoPi;
+        }
+    }
+    return cuda_status(nabla_launch_rope(a, p->dtype, p->layout, wide, as_stream(stream)));
+}
+
+size_t nabla_packed_workspace_size(const nabla_packed *shape, int op) {
+    if (shape == nullptr || !packed_shape_ok(shape) ||
+        (op != NABLA_PACKED_FWD && op != NABLA_PACKED_BWD))
+        return 0;
+    return packed_ws(shape, op);
+}
+
+int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const nabla_view *k,
+                          const nabla_view *v, const int32_t *cu_q, const int32_t *cu_k,
+                          const nabla_view *o, float *lse, void *workspace, size_t workspace_bytes,
+                          nabla_stream_t stream) {
+    int st = check_packed(shape, cu_q, cu_k, NABLA_PACKED_FWD, workspace, workspace_bytes);
+    if (st != NABLA_OK) return st;
+    Box bq, bk, bv, bo;
+    if ((st = packed_view(q, shape->total_q, shape->heads, shape->D, false, &bq)) != NABLA_OK ||
+        (st = packed_view(k, shape->total_k, shape->heads_kv, shape->D, false, &bk)) != NABLA_OK ||
+        (st = packed_view(v, shape->total_k, shape->heads_kv, shape->D, false, &bv)) != NABLA_OK ||
+        (st = packed_view(o, shape->total_q, shape->heads, shape->D, true, &bo)) != NABLA_OK)
+        return st;
+    if (shape->total_q > 0 && (!disjoint(bo, bq) || (shape->total_k > 0 &&
+                                                     (!disjoint(bo, bk) || !disjoint(bo, bv)))))
+        return NABLA_ERR_PARAM;
+    const int64_t units = fwd_units(shape);
+    if (units > INT32_MAX) return NABLA_ERR_SHAPE;
+    cudaStream_t s = as_stream(stream);
+    if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return NABLA_ERR_CUDA;
+    if (shape->total_q == 0) return NABLA_OK;
+    nabla::packed::Args a = packed_args(shape, cu_q, cu_k, workspace);
+    a.q = dev_view(q);
+    a.k = dev_view(k);
+    a.v = dev_view(v);
+    a.o = dev_view(o);
+    a.lse = lse;
+    a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kStatusBytes);
+    return cuda_status(nabla_launch_packed_fwd(a, shape->D, units, fwd_splits(shape), s));
+}
+
+int nabla_cache_append(const nabla_cache *cache, const nabla_view *k, const nabla_view *v,
+                       int64_t total, const int32_t *starts, const int32_t *cu, void *workspace,
+                       size_t workspace_bytes, nabla_stream_t stream) {
+    if (cache == nullptr || k == nullptr || v == nullptr) return NABLA_ERR_NULL;
+    if (!cache_shape_ok(cache) || total < 0 || total > INT32_MAX) return NABLA_ERR_SHAPE;
+    if (cu == nullptr && total != cache->seqs) return NABLA_ERR_SHAPE;  // one row a sequence
+    nabla::AppendArgs a = {};
+    if (workspace != nullptr) {
+        const int st = check_workspace(workspace, workspace_bytes, kStatusBytes);
+        if (st != NABLA_OK) return st;
+        a.status = static_cast<int *>(workspace);
+    }
+    Box pool[2], bk, bv;
+    const bool work = total > 0 && cache->seqs > 0;
+    if (work) {
+        const int st = check_cache(cache, true, pool, &a.c);
+        if (st != NABLA_OK) return st;
+        if (k->data == nullptr || v->data == nullptr || starts == nullptr) return NABLA_ERR_NULL;
+        if (((reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(cu)) & 3u) != 0)
+            return NABLA_ERR_ALIGN;
+        if (!make_box(k, 1, cache->heads_kv, total, cache->D, 2, &bk) ||
+            !make_box(v, 1, cache->heads_kv, total, cache->D, 2, &bv))
+            return NABLA_ERR_PARAM;
+        if (!multiple_of_16(bk) || !multiple_of_16(bv)) return NABLA_ERR_ALIGN;
+        // rows that lie in the pool itself could be overwritten before they are read;
+        // K and V of one pool are views of one buffer, so only their rows may not coincide
+        for (const Box &p : pool)
+            if (!(bk.hi <= p.lo || p.hi <= bk.lo) || !(bv.hi <= p.lo || p.hi <= bv.lo))
+                return NABLA_ERR_PARAM;
+        if (same_view(pool[0], pool[1])) return NABLA_ERR_PARAM;
+    }
+    cudaStream_t s = as_stream(stream);
+    if (workspace != nullptr && cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess)
+        return NABLA_ERR_CUDA;
+    if (!work) return NABLA_OK;
+    a.k = static_cast<const __nv_bfloat16 *>(k->data);
+    a.v = static_cast<const __nv_bfloat16 *>(v->data);
+    a.k_head = bk.stride[1];
+    a.k_token = bk.stride[2];
+    a.v_head = bv.stride[1];
+    a.v_token = bv.stride[2];
+    a.starts = starts;
+    a.cu = cu;
+    a.total = total;
+    return cuda_status(nabla_launch_append(a, s));
+}
+
+size_t nabla_paged_workspace_size(const nabla_cache *cache, int heads) {
+    if (cache == nullptr || !cache_shape_ok(cache) || (cache->D != 64 && cache->D != 128) ||
+        heads < 1 || heads % cache->heads_kv != 0)
+        return 0;
+    return paged_ws(cache);
+}
+
+int nabla_attn_paged(const nabla_cache *cache, int heads, float scale, const nabla_view *q,
+                     const int32_t *lens, const nabla_view *o, float *lse, void *workspace,
+                     size_t workspace_bytes, nabla_stream_t stream) {
+    if (cache == nullptr || q == nullptr || o == nullptr) return NABLA_ERR_NULL;
+    if (nabla_paged_workspace_size(cache, heads) == 0) return NABLA_ERR_SHAPE;
+    if (static_cast<int64_t>(cache->seqs) * heads > INT32_MAX) return NABLA_ERR_SHAPE;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return NABLA_ERR_PARAM;
+    int st = check_workspace(workspace, workspace_bytes, paged_ws(cache));
+    if (st != NABLA_OK) return st;
+    cudaStream_t s = as_stream(stream);
+    if (cache->seqs == 0)
+        return cuda_status(cudaMemsetAsync(workspace, 0, sizeof(int), s));
+    nabla::PagedArgs a = {};
+    Box pool[2], bq, bo;
+    if ((st = check_cache(cache, false, pool, &a.c)) != NABLA_OK) return st;
+    if (q->data == nullptr || o->data == nullptr || lens == nullptr) return NABLA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(lens) & 3u) != 0) return NABLA_ERR_ALIGN;
+    if (!make_box(q, 1, heads, cache->seqs, cache->D, 2, &bq) ||
+        !make_box(o, 1, heads, cache->seqs, cache->D, 2, &bo))
+        return NABLA_ERR_PARAM;
+    if (!multiple_of_16(bq) || !multiple_of_16(bo)) return NABLA_ERR_ALIGN;
+    if (!self_disjoint(bo) || !disjoint(bo, bq) || !disjoint(bo, pool[0]) || !disjoint(bo, pool[1]))
+        return NABLA_ERR_PARAM;
+    a.q = static_cast<const __nv_bfloat16 *>(q->data);
+    a.o = static_cast<__nv_bfloat16 *>(o->data);
+    a.q_head = bq.stride[1];
+    a.q_token = bq.stride[2];
+    a.o_head = bo.stride[1];
+    a.o_token = bo.stride[2];
+    a.lens = lens;
+    a.lse = lse;
+    unsigned char *w = static_cast<unsigned char *>(workspace);
+    a.status = reinterpret_cast<int *>(w);
+    a.flags = reinterpret_cast<int *>(w + kStatusBytes);
+    a.part = reinterpret_cast<float *>(w + kStatusBytes + round256(sizeof(int) * nabla::kPagedCtas));
+    a.c2 = scale * 1.4426950408889634f;
+    a.heads = heads;
+    a.group = heads / cache->heads_kv;
+    a.chunks = (a.group + nabla::kPagedHeads - 1) / nabla::kPagedHeads;
+    a.ctas = nabla::kPagedCtas;
+    return cuda_status(nabla_launch_paged(a, s));
+}
+
+}  // extern "C"

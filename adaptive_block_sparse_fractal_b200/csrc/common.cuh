@@ -12,6 +12,7 @@ constexpr int kBlk = 64;  // tokens per block: one 8 x 8 patch of one frame
 // Device status codes written into the workspace status word.
 constexpr int kDevOk = 0;
 constexpr int kDevTimeout = 1;
+constexpr int kDevParam = 2;  // device-side input (borders, lengths, page numbers) out of range
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

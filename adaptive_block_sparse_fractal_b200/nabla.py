@@ -4,6 +4,7 @@ Argument marshalling only: torch tensors provide device memory and the
 current CUDA stream; every step runs in the library's kernels.  There is no
 fallback: if the library is missing or a call fails, this module raises.
 """
+import contextlib
 import ctypes
 import os
 
@@ -22,8 +23,15 @@ MASK_BITS, MASK_ROW_IDX, MASK_ROW_CNT, MASK_COL_IDX, MASK_COL_CNT, MASK_SCORES =
 # every symbol include/nabla.h declares
 SYMBOLS = ("nabla_flatten", "nabla_workspace_size", "nabla_mask_bytes", "nabla_build_mask",
            "nabla_build_mask_grid", "nabla_build_mask_static", "nabla_build_mask_dr",
-           "nabla_attn_fwd", "nabla_attn_bwd", "nabla_status", "nabla_strerror")
+           "nabla_attn_fwd", "nabla_attn_bwd", "nabla_status", "nabla_strerror",
+           "nabla_rope", "nabla_packed_workspace_size", "nabla_attn_packed_fwd",
+           "nabla_cache_append", "nabla_paged_workspace_size",
+           "nabla_attn_paged")
 DR_STATIC_RATIO, DR_THRESHOLD = 0, 1
+ROPE_ADJACENT, ROPE_HALVES = 0, 1
+ROPE_INVERSE, ROPE_FLAT_IN, ROPE_FLAT_OUT = 1, 2, 4
+PACKED_FWD, PACKED_BWD = 0, 1
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 class NablaError(RuntimeError):
@@ -52,6 +60,30 @@ class MaskStruct(ctypes.Structure):
                 for n in ("bits", "row_idx", "row_cnt", "col_idx", "col_cnt", "scores")]
 
 
+class View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
+                ("token", ctypes.c_int64)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("layout", ctypes.c_int), ("D", ctypes.c_int),
+                ("pairs", ctypes.c_int * 3), ("theta", ctypes.c_double * 3),
+                ("scale", ctypes.c_double * 3), ("offset", ctypes.c_double * 3),
+                ("flags", ctypes.c_uint)]
+
+
+class Packed(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int), ("heads", ctypes.c_int), ("heads_kv", ctypes.c_int),
+                ("D", ctypes.c_int), ("total_q", ctypes.c_int64), ("total_k", ctypes.c_int64),
+                ("causal", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", View), ("v", View), ("table", ctypes.c_void_p), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads_kv", ctypes.c_int), ("D", ctypes.c_int),
+                ("seqs", ctypes.c_int), ("table_width", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -64,6 +96,7 @@ def lib():
                                "`python -m adaptive_block_sparse_fractal_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+        F = ctypes.c_float
         L.nabla_flatten.argtypes = [P, P, I64, I, I, I, I, I64, I, P]
         L.nabla_flatten.restype = I
         L.nabla_workspace_size.argtypes = [P, I]
@@ -86,6 +119,18 @@ def lib():
         L.nabla_status.restype = I
         L.nabla_strerror.argtypes = [I]
         L.nabla_strerror.restype = ctypes.c_char_p
+        L.nabla_rope.argtypes = [P, I, I, I, I, I, I, P, P, P, P, I64, I, P]
+        L.nabla_rope.restype = I
+        L.nabla_packed_workspace_size.argtypes = [P, I]
+        L.nabla_packed_workspace_size.restype = SZ
+        L.nabla_attn_packed_fwd.argtypes = [P, P, P, P, P, P, P, P, P, SZ, P]
+        L.nabla_attn_packed_fwd.restype = I
+        L.nabla_cache_append.argtypes = [P, P, P, I64, P, P, P, SZ, P]
+        L.nabla_cache_append.restype = I
+        L.nabla_paged_workspace_size.argtypes = [P, I]
+        L.nabla_paged_workspace_size.restype = SZ
+        L.nabla_attn_paged.argtypes = [P, I, F, P, P, P, P, P, SZ, P]
+        L.nabla_attn_paged.restype = I
         _lib = L
     return _lib
 
@@ -265,6 +310,245 @@ def attn_bwd(shape, params, q, k, v, o, dout, lse, mask, dq=None, dk=None, dv=No
                                 _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(), _stream(q)),
            "nabla_attn_bwd")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# rotary positions, packed-sequence attention, the paged cache
+# ---------------------------------------------------------------------------
+_no_change = contextlib.nullcontext()
+
+
+def _on(t):
+    """The tensor's device as the current one (the library launches there)."""
+    if torch.cuda.current_device() == t.device.index:
+        return _no_change
+    return torch.cuda.device(t.device)
+
+
+def _rows(t, dims, dtype, name, like=None):
+    """A CUDA tensor of `dims` dimensions whose rows are contiguous."""
+    if not (t.is_cuda and t.dtype == dtype and t.dim() == dims):
+        raise ValueError("%s must be a CUDA %s tensor of %d dimensions" % (name, dtype, dims))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s: the last dimension must be contiguous" % name)
+    if like is not None and t.device != like.device:
+        raise ValueError("%s must be on %s" % (name, like.device))
+    return t
+
+
+def _ints(t, shape, name, like):
+    if not (t.is_cuda and t.dtype == torch.int32 and t.is_contiguous() and t.device == like.device):
+        raise ValueError("%s must be a contiguous int32 tensor on %s" % (name, like.device))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    return t
+
+
+def _same(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _work(ws, like):
+    if not (ws.is_cuda and ws.device == like.device and ws.dtype == torch.uint8 and
+            ws.is_contiguous()):
+        raise ValueError("ws must be a contiguous uint8 tensor on %s" % like.device)
+    return ws
+
+
+def _tokens(t):
+    """Reference to the view of a [tokens, heads, D] tensor."""
+    return ctypes.byref(View(t.data_ptr(), 0, t.stride(1), t.stride(0)))
+
+
+def rope_params_of(pairs, theta=10000.0, scale=1.0, offset=0.0, layout=ROPE_ADJACENT,
+                   inverse=False):
+    """Rotary parameters: `pairs` turned by each of up to three axes (time,
+    height, width); theta, scale and offset are one number or one per axis.
+    dtype, D and the token order are filled in by rope()."""
+    pairs = [int(n) for n in pairs]
+    if not 1 <= len(pairs) <= 3:
+        raise ValueError("pairs: one to three axes")
+
+    def axes(x):
+        x = [float(v) for v in x] if isinstance(x, (tuple, list)) else [float(x)] * len(pairs)
+        return tuple(x[:3]) + (1.0,) * (3 - len(x[:3]))
+    p = RopeParams()
+    p.layout = int(layout)
+    p.pairs = tuple(pairs) + (0,) * (3 - len(pairs))
+    p.theta, p.scale, p.offset = axes(theta), axes(scale), axes(offset)
+    p.flags = ROPE_INVERSE if inverse else 0
+    return p
+
+
+def rope(params, q, k=None, grid=None, pos=None, flat_in=False, flat_out=False, P=8, q_out=None,
+         k_out=None):
+    """Rotate q, or q and k ([B, heads, N, D] or [heads, N, D], any strides with
+    contiguous rows; bf16, fp16 or fp32) by the positions of a (T, H, W) grid or
+    by `pos` (int32 [N, axes] or [B, N, axes], in grid order).  flat_in /
+    flat_out: that side is in flattened token order (needs `grid`).  Outputs may
+    be the inputs (same order on both sides).  Returns q_out, or (q_out, k_out)."""
+    dims = q.dim()
+    if dims not in (3, 4) or q.dtype not in DTYPES:
+        raise ValueError("q must be [B, heads, N, D] or [heads, N, D] in bf16, fp16 or fp32")
+    N, D = q.shape[-2:]
+    B = q.shape[0] if dims == 4 else 1
+    if grid is None:
+        if pos is None or flat_in or flat_out:
+            raise ValueError("grid is needed without pos and for a flattened order")
+        grid = (N, 1, 1)
+    T, H, W = (int(n) for n in grid)
+    if T * H * W != N:
+        raise ValueError("grid %s does not hold %d tokens" % (tuple(grid), N))
+    ins = [q] if k is None else [q, k]
+    outs = [q_out] if k is None else [q_out, k_out]
+    heads = (ctypes.c_int * 2)()
+    vi, vo = (View * 2)(), (View * 2)()
+    for i, x in enumerate(ins):
+        _rows(x, dims, q.dtype, "qk"[i], q)
+        if x.shape[-2:] != q.shape[-2:] or (dims == 4 and x.shape[0] != B):
+            raise ValueError("q and k must have the same batch, tokens and D")
+        if outs[i] is None:
+            outs[i] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _rows(outs[i], dims, q.dtype, "qk"[i] + "_out", q)
+        _same(y, x.shape, "qk"[i] + "_out")
+        heads[i] = x.shape[-3]
+        for t, v in ((x, vi[i]), (y, vo[i])):
+            v.data, v.batch = t.data_ptr(), t.stride(0) if dims == 4 else 0
+            v.head, v.token = t.stride(-3), t.stride(-2)
+    pos_batch, axes = 0, 0
+    if pos is not None:
+        axes = pos.shape[-1]
+        _ints(pos, (N, axes) if pos.dim() == 2 else (B, N, axes), "pos", q)
+        pos_batch = N * axes if pos.dim() == 3 else 0
+    p = RopeParams.from_buffer_copy(params)
+    p.dtype, p.D = DTYPES[q.dtype], D
+    p.flags |= (ROPE_FLAT_IN if flat_in else 0) | (ROPE_FLAT_OUT if flat_out else 0)
+    with _on(q):
+        _check(lib().nabla_rope(ctypes.byref(p), B, T, H, W, int(P), len(ins), heads, vi, vo,
+                                _ptr(pos), pos_batch, axes, _stream(q)), "nabla_rope")
+    return outs[0] if k is None else (outs[0], outs[1])
+
+
+def _packed_of(q, k, v, cu_q, cu_k, causal, scale):
+    _rows(q, 3, torch.bfloat16, "q")
+    _rows(k, 3, torch.bfloat16, "k", q)
+    _rows(v, 3, torch.bfloat16, "v", q)
+    _same(v, k.shape, "v")
+    if k.shape[2] != q.shape[2]:
+        raise ValueError("q and k must have the same D")
+    _ints(cu_q, (cu_q.numel(),), "cu_q", q)
+    _ints(cu_k, cu_q.shape, "cu_k", q)
+    D = q.shape[2]
+    return Packed(cu_q.numel() - 1, q.shape[1], k.shape[1], D, q.shape[0], k.shape[0],
+                  int(bool(causal)), float(D ** -0.5 if scale is None else scale))
+
+
+def packed_workspace(q, k, seqs, back=False):
+    """Workspace of the packed calls for q [total_q, heads, D], k [total_k,
+    heads_kv, D] and `seqs` sequences; back=True serves both directions.  It
+    serves one call at a time."""
+    s = Packed(int(seqs), q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], 0, 1.0)
+    n = int(lib().nabla_packed_workspace_size(ctypes.byref(s), PACKED_BWD if back else PACKED_FWD))
+    if n == 0:
+        raise NablaError(ERR_SHAPE, "nabla_packed_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def attn_packed_fwd(q, k, v, cu_q, cu_k, causal=False, scale=None, o=None, lse=None, ws=None,
+                    want_lse=True):
+    """Attention of packed sequences: q [total_q, heads, D], k, v [total_k,
+    heads_kv, D] (bf16, any strides of 16 bytes with contiguous rows), borders
+    cu_q, cu_k int32 [seqs + 1].  causal aligns the last rows of q and k.
+    Returns o [total_q, heads, D] and lse float32 [heads, total_q]; rows of no
+    sequence are left as they were."""
+    s = _packed_of(q, k, v, cu_q, cu_k, causal, scale)
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+    _same(_rows(o, 3, torch.bfloat16, "o", q), q.shape, "o")
+    if lse is None and want_lse:
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        _same(lse, (q.shape[1], q.shape[0]), "lse")
+    ws = packed_workspace(q, k, s.seqs) if ws is None else _work(ws, q)
+    with _on(q):
+        _check(lib().nabla_attn_packed_fwd(ctypes.byref(s), _tokens(q), _tokens(k), _tokens(v),
+                                           _ptr(cu_q), _ptr(cu_k), _tokens(o), _ptr(lse), _ptr(ws),
+                                           ws.numel(), _stream(q)), "nabla_attn_packed_fwd")
+    return o, lse
+
+
+def _cache_of(k_cache, v_cache, table, seqs):
+    _rows(k_cache, 4, torch.bfloat16, "k_cache")
+    _rows(v_cache, 4, torch.bfloat16, "v_cache", k_cache)
+    _same(v_cache, k_cache.shape, "v_cache")
+    pages, page, heads_kv, D = k_cache.shape
+    if table is not None:
+        _ints(table, (seqs, table.shape[-1]), "table", k_cache)
+    kv = [View(t.data_ptr(), t.stride(0), t.stride(2), t.stride(1)) for t in (k_cache, v_cache)]
+    return Cache(kv[0], kv[1], _ptr(table), pages, page, heads_kv, D, seqs,
+                 1 if table is None else table.shape[1])
+
+
+def cache_workspace(device):
+    """Workspace of cache_append (its status word)."""
+    return torch.empty(256, dtype=torch.uint8, device=device)
+
+
+def cache_append(k, v, k_cache, v_cache, table, starts, cu=None, ws=None):
+    """Write rows k, v [total, heads_kv, D] of packed sequences (borders cu
+    [seqs + 1]; None: one row each) into the pages [pages, page_size, heads_kv,
+    D] behind the starts[s] rows that sequence s has.  table int32 [seqs,
+    width].  Rows without a page are skipped; with `ws` (cache_workspace) they
+    are reported by status(ws)."""
+    seqs = starts.numel()
+    _ints(starts, (seqs,), "starts", k)
+    if cu is not None:
+        _ints(cu, (seqs + 1,), "cu", k)
+    c = _cache_of(k_cache, v_cache, table, seqs)
+    for t, n in ((k, "k"), (v, "v")):
+        _same(_rows(t, 3, torch.bfloat16, n, k_cache), (k.shape[0], c.heads_kv, c.D), n)
+    with _on(k):
+        _check(lib().nabla_cache_append(ctypes.byref(c), _tokens(k), _tokens(v), k.shape[0],
+                                        _ptr(starts), _ptr(cu),
+                                        None if ws is None else _ptr(_work(ws, k)),
+                                        0 if ws is None else ws.numel(), _stream(k)),
+               "nabla_cache_append")
+
+
+def paged_workspace(q, k_cache):
+    """Workspace of attn_paged; it serves one call at a time."""
+    c = _cache_of(k_cache, k_cache, None, 0)
+    n = int(lib().nabla_paged_workspace_size(ctypes.byref(c), q.shape[1]))
+    if n == 0:
+        raise NablaError(ERR_SHAPE, "nabla_paged_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def attn_paged(q, k_cache, v_cache, table, lens, scale=None, o=None, lse=None, ws=None,
+               want_lse=True):
+    """Attention of one new token per sequence, q [seqs, heads, D], over the
+    first lens[s] rows of its pages.  Returns o and lse float32 [seqs, heads]."""
+    _rows(q, 3, torch.bfloat16, "q", k_cache)
+    seqs, heads, D = q.shape
+    c = _cache_of(k_cache, v_cache, table, seqs)
+    if c.D != D:
+        raise ValueError("q and the cache must have the same D")
+    _ints(lens, (seqs,), "lens", q)
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+    _same(_rows(o, 3, torch.bfloat16, "o", q), q.shape, "o")
+    if lse is None and want_lse:
+        lse = torch.empty((seqs, heads), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        _same(lse, (seqs, heads), "lse")
+    ws = paged_workspace(q, k_cache) if ws is None else _work(ws, q)
+    with _on(q):
+        _check(lib().nabla_attn_paged(ctypes.byref(c), heads,
+                                      float(D ** -0.5 if scale is None else scale), _tokens(q),
+                                      _ptr(lens), _tokens(o), _ptr(lse), _ptr(ws), ws.numel(),
+                                      _stream(q)), "nabla_attn_paged")
+    return o, lse
 
 
 def status(ws):

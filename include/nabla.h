@@ -282,8 +282,135 @@ int nabla_attn_bwd(const nabla_shape *shape, const nabla_params *params, const n
                    nabla_bf16 *dq, nabla_bf16 *dk, nabla_bf16 *dv, void *workspace,
                    size_t workspace_bytes, nabla_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the grid attention: rotary positions for its q and k, dense attention
+ * of packed sequences (text prompts, cross attention to them, clips of
+ * different lengths) and attention over a paged key-value cache.  (No
+ * counterpart on the page.)  The conventions above hold, and:
+ *   - tensors are views: a base pointer and the distances in ELEMENTS between
+ *     neighbouring batch entries, heads and tokens; the D features of a row are
+ *     contiguous.  Distances of dimensions of size one are not looked at.
+ *   - sequence borders, positions, lengths and page numbers are device memory
+ *     and so unknown to the host; each call says what it does with bad ones.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void *data;
+    int64_t batch, head, token;
+} nabla_view;
+
+/* element types of nabla_rope */
+#define NABLA_BF16 0
+#define NABLA_FP16 1
+#define NABLA_FP32 2
+
+/* which features form a rotated pair, with R = pairs[0] + pairs[1] + pairs[2] */
+#define NABLA_ROPE_ADJACENT 0 /* pair i = features (2i, 2i + 1) */
+#define NABLA_ROPE_HALVES 1   /* pair i = features (i, i + R)   */
+
+/* nabla_rope_params.flags */
+#define NABLA_ROPE_INVERSE 1u  /* rotate by the negative angle: the inverse and the gradient */
+#define NABLA_ROPE_FLAT_IN 2u  /* inputs in flattened order  */
+#define NABLA_ROPE_FLAT_OUT 4u /* outputs in flattened order */
+
+/* Rotary positions on up to three axes (time, height, width).
+ *   pairs   pairs rotated by each axis, in this order; 2 R <= D, the features
+ *           behind the rotated ones are copied.  0 leaves an axis out.
+ *   theta, scale, offset   the pair i of axis a turns by
+ *           (position_a + offset[a]) * scale[a] * theta[a]^(-i / pairs[a]),
+ *           taken in float64 before its sine and cosine. */
+typedef struct {
+    int dtype, layout, D;
+    int pairs[3];
+    double theta[3], scale[3], offset[3];
+    unsigned flags;
+} nabla_rope_params;
+
+/* Rotates `count` tensors (1 or 2: q alone, or q and k) of B batch entries,
+ * heads[i] heads and N = T*H*W tokens in one pass:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * in float32, rounded once to dtype.  The axes are a token's frame, row and
+ * column, or with `pos` (int32 [B or 1, N, pos_axes], in grid order; pos_batch =
+ * distance between batch entries, 0 to share them) its pos_axes given
+ * positions.  NABLA_ROPE_FLAT_IN / _OUT read or write the token order of
+ * nabla_flatten (H and W multiples of P), so that rotation and flattening are
+ * one pass; the gradient of a flattening call is the call with _INVERSE and
+ * _IN / _OUT exchanged.
+ * D even, 2 <= D <= 256.  Views whose pointers and distances are multiples of
+ * 16 bytes (and, in the HALVES layout, R a multiple of the elements in 16 bytes)
+ * take 16-byte accesses; any other view is accepted as long as its pointers are
+ * aligned to its elements.  An output may be its own input (same view, same
+ * order); otherwise no output may overlap an input or another output
+ * (NABLA_ERR_PARAM). */
+int nabla_rope(const nabla_rope_params *params, int B, int T, int H, int W, int P, int count,
+               const int *heads, const nabla_view *in, const nabla_view *out, const int32_t *pos,
+               int64_t pos_batch, int pos_axes, nabla_stream_t stream);
+
+/* Attention of packed sequences.  q, o, dout, dq are [total_q, heads, D] and k,
+ * v, dk, dv [total_k, heads_kv, D] bf16 views (batch unused); sequence s is rows
+ * cu_q[s] .. cu_q[s+1]-1 of q and cu_k[s] .. cu_k[s+1]-1 of k, v (int32
+ * [seqs + 1] each, ascending from >= 0; the two may be one array).  heads is a
+ * multiple of heads_kv: query head h reads key head h / (heads / heads_kv).
+ *   causal  row i of Lq keeps the keys j <= i + Lk - Lq of its sequence (the
+ *           last rows of both coincide); otherwise it keeps all of them.
+ * Rows of q and k that belong to no sequence are neither read into a result nor
+ * written.  D in {64, 128}; pointers and distances multiples of 16 bytes.
+ * Borders that do not ascend, or that leave [0, total], make the call write
+ * NABLA_ERR_PARAM to the workspace status and leave the outputs unwritten. */
+typedef struct {
+    int seqs, heads, heads_kv, D;
+    int64_t total_q, total_k;
+    int causal;
+    float scale;
+} nabla_packed;
+
+#define NABLA_PACKED_FWD 0
+#define NABLA_PACKED_BWD 1 /* also serves the forward */
+/* Bytes of workspace of the packed calls (0 for invalid sizes). */
+size_t nabla_packed_workspace_size(const nabla_packed *shape, int op);
+
+/* o = softmax(scale q k^T) v over the kept keys (fp32 accumulate) and lse
+ * (float32 [heads, total_q], may be NULL).  A row that keeps no key gets o = 0
+ * and lse = -inf. */
+int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const nabla_view *k,
+                          const nabla_view *v, const int32_t *cu_q, const int32_t *cu_k,
+                          const nabla_view *o, float *lse, void *workspace, size_t workspace_bytes,
+                          nabla_stream_t stream);
+
+/* A paged key-value cache: k and v are pools of `pages` pages of page_size
+ * rows, heads_kv heads and D features (bf16; batch = distance between pages).
+ * Row p of sequence s is row p % page_size of page
+ * table[s * table_width + p / page_size]. */
+typedef struct {
+    nabla_view k, v;
+    const int32_t *table;
+    int pages, page_size, heads_kv, D, seqs, table_width;
+} nabla_cache;
+
+/* Writes rows k, v ([total, heads_kv, D] views) of packed sequences behind
+ * their first starts[s] rows: token i of sequence s (cu[s] <= row < cu[s+1];
+ * cu may be NULL for one token each, total = seqs) goes to row starts[s] + i.
+ * A row that falls outside the table or on a page outside the pool is skipped
+ * and, when a workspace (256 bytes) is given, reported as NABLA_ERR_PARAM in its
+ * status; with workspace NULL it is skipped silently.  Two sequences must not
+ * write the same page rows in one call.  D a multiple of 8, 16-byte views. */
+int nabla_cache_append(const nabla_cache *cache, const nabla_view *k, const nabla_view *v,
+                       int64_t total, const int32_t *starts, const int32_t *cu, void *workspace,
+                       size_t workspace_bytes, nabla_stream_t stream);
+
+/* Attention of one new token of each sequence over lens[s] cached rows:
+ * q, o [seqs, heads, D] views (token = distance between sequences), lse float32
+ * [seqs, heads] or NULL.  lens[s] = 0 gives o = 0, lse = -inf.  A length outside
+ * [0, table_width * page_size] counts as 0 and a page outside the pool as masked;
+ * both are reported as NABLA_ERR_PARAM in the workspace status.
+ * D in {64, 128}.  Deterministic for given lengths. */
+size_t nabla_paged_workspace_size(const nabla_cache *cache, int heads);
+int nabla_attn_paged(const nabla_cache *cache, int heads, float scale, const nabla_view *q,
+                     const int32_t *lens, const nabla_view *o, float *lse, void *workspace,
+                     size_t workspace_bytes, nabla_stream_t stream);
+
 /* Synchronises `stream`, then returns the device-side status recorded in the
- * workspace by the last call that used it (NABLA_OK or NABLA_ERR_TIMEOUT),
+ * workspace by the last call that used it (NABLA_OK, NABLA_ERR_TIMEOUT, or
+ * NABLA_ERR_PARAM for the device-side inputs of the packed and cache calls),
  * or NABLA_ERR_CUDA if the stream reports an error. */
 int nabla_status(const void *workspace, nabla_stream_t stream);
 

@@ -1,0 +1,176 @@
+"""Packed-sequence attention against float64 (bounds derived in seq_util.py)."""
+import math
+
+import pytest
+import torch
+
+from adaptive_block_sparse_fractal_b200 import nabla
+
+import seq_util
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def borders(lens, first=0):
+    out = [first]
+    for n in lens:
+        out.append(out[-1] + n)
+    return out
+
+
+def make(lens_q, lens_k, heads, heads_kv, D, seed=0, behind=0, std=1.0):
+    """Packed inputs with `behind` NaN rows behind the last sequence."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    cq, ck = borders(lens_q), borders(lens_k)
+
+    def t(n, h):
+        x = (torch.randn(n + behind, h, D, generator=g, device="cuda") * std).to(BF)
+        x[n:] = math.nan
+        return x
+    q, k, v, dout = t(cq[-1], heads), t(ck[-1], heads_kv), t(ck[-1], heads_kv), t(cq[-1], heads)
+    dev = lambda c: torch.tensor(c, dtype=torch.int32, device="cuda")
+    return q, k, v, dout, cq, ck, dev(cq), dev(ck)
+
+
+def run_fwd(q, k, v, cu_q, cu_k, causal, **kw):
+    ws = nabla.packed_workspace(q, k, cu_q.numel() - 1)
+    o = torch.full(q.shape, 7.0, dtype=BF, device="cuda")
+    lse = torch.full((q.shape[1], q.shape[0]), 7.0, device="cuda")
+    nabla.attn_packed_fwd(q, k, v, cu_q, cu_k, causal=causal, o=o, lse=lse, ws=ws, **kw)
+    assert nabla.status(ws) == nabla.OK
+    return o, lse
+
+
+CASES = [
+    # lens_q, lens_k, heads, heads_kv
+    ([1], [1], 1, 1),
+    ([1, 1, 1], [1, 2, 129], 2, 1),
+    ([128], [128], 1, 1),
+    ([129, 127], [127, 130], 2, 2),
+    ([257, 0, 3], [257, 5, 0], 3, 1),
+    ([77, 1, 200, 33], [77, 1, 200, 33], 6, 2),
+    ([600, 511], [600, 1000], 5, 1),
+    ([5, 300], [1500, 40], 4, 4),   # row tiles against many and few keys
+    ([100], [30], 8, 2),            # causal: 70 rows keep nothing
+    ([64, 64, 64, 64, 64], [0, 64, 1, 128, 63], 7, 1),
+    ([1000], [1000], 10, 2),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D", [128, 64])
+def test_forward(case, causal, D):
+    lens_q, lens_k, hq, hk = CASES[case]
+    q, k, v, _, cq, ck, dq_, dk_ = make(lens_q, lens_k, hq, hk, D, seed=case, behind=70)
+    o, lse = run_fwd(q, k, v, dq_, dk_, causal)
+    r = seq_util.packed(q, k, v, cq, ck, causal)
+    n = cq[-1]
+    assert bool((o[n:] == 7).all()) and bool((lse[:, n:] == 7).all())  # rows of no sequence
+    seq_util.check(o[:n], r["o"][:n], r["o_tol"][:n], "o")
+    seq_util.check_lse(lse[:, :n], r["lse"][:, :n])
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_forward_split_over_keys(D):
+    """Few rows, many keys: the key range is split and joined."""
+    for lens_q, lens_k, hq, hk, causal in (([1], [9000], 2, 1, True), ([3, 1], [4100, 6001], 4, 2, True),
+                                           ([40], [8192], 6, 2, False), ([2, 0, 5], [5000, 4000, 0], 2, 2, True)):
+        q, k, v, _, cq, ck, dq_, dk_ = make(lens_q, lens_k, hq, hk, D, seed=5, behind=3)
+        o, lse = run_fwd(q, k, v, dq_, dk_, causal)
+        r = seq_util.packed(q, k, v, cq, ck, causal)
+        n = cq[-1]
+        assert bool((o[n:] == 7).all()) and bool((lse[:, n:] == 7).all())
+        seq_util.check(o[:n], r["o"][:n], r["o_tol"][:n], "o")
+        seq_util.check_lse(lse[:, :n], r["lse"][:, :n])
+
+
+def test_forward_rising_scores_and_scale():
+    """Maxima that grow by far more than the rescaling headroom along the keys."""
+    L, D = 700, 128
+    q, k, v, _, cq, ck, cu, _ = make([L], [L], 2, 2, D, seed=3)
+    k *= torch.linspace(0.01, 6, L, device="cuda")[:, None, None]
+    k = k.to(BF)
+    for causal in (False, True):
+        o, lse = run_fwd(q, k, v, cu, cu, causal, scale=0.25)
+        r = seq_util.packed(q, k, v, cq, ck, causal, scale=0.25)
+        # scores reach a few hundred here: their float32 error enters the exponent
+        x = float(r["lse"].abs().max())
+        seq_util.check(o, r["o"], r["o_tol"] + x * 2.0 ** -20 * r["o_tol"] / seq_util.H, "o")
+        seq_util.check(lse, r["lse"], 2.0 ** -20 * (1 + r["lse"].abs()) + 2.0 ** -18, "lse")
+
+
+def test_neighbouring_sequences_do_not_leak():
+    """NaN and infinities in the sequences around one, in the padding behind the
+    last and in the gap in front of the first leave its rows alone."""
+    D, hq, hk = 128, 4, 2
+    q, k, v, _, _, _, _, _ = make([400], [400], hq, hk, D, seed=9)
+    cu = torch.tensor([10, 100, 230, 390], dtype=torch.int32, device="cuda")
+    for t in (q, k, v):
+        t[:10], t[390:] = math.nan, math.nan
+        t[10:100], t[230:390] = math.inf, math.nan
+    for causal in (False, True):
+        o, lse = run_fwd(q, k, v, cu, cu, causal)
+        r = seq_util.packed(q, k, v, [100, 230], [100, 230], causal)
+        seq_util.check(o, r["o"], r["o_tol"], "o")
+        seq_util.check_lse(lse, r["lse"])
+        assert bool((o[:10] == 7).all()) and bool((o[390:] == 7).all())
+
+
+def test_strides_and_layouts():
+    """Slices of one fused projection, heads in front, padded rows."""
+    L, hq, hk, D = 150, 4, 2, 64
+    qkv = torch.randn(L, hq + 2 * hk, D, device="cuda").to(BF)
+    cu = torch.tensor([0, 70, L], dtype=torch.int32, device="cuda")
+    a, b, c = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    o, lse = run_fwd(a, b, c, cu, cu, True)
+    r = seq_util.packed(a, b, c, [0, 70, L], [0, 70, L], True)
+    seq_util.check(o, r["o"], r["o_tol"], "o")
+    first = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)
+    wide = torch.randn(L, hk, D + 8, device="cuda").to(BF)
+    wide[:, :, :D] = b
+    out = torch.full((hq, L + 5, D), 7.0, device="cuda").to(BF)
+    view = out[:, :L].transpose(0, 1)
+    got, lse2 = nabla.attn_packed_fwd(first(a), wide[:, :, :D], first(c), cu, cu, causal=True, o=view)
+    assert torch.equal(got, o) and torch.equal(lse2, lse)
+    assert bool((out[:, L:] == 7).all())
+
+
+@pytest.mark.parametrize("cq,ck", [([0, 50, 40], [0, 10, 20]), ([0, 10, 101], [0, 10, 20]),
+                                   ([-1, 10, 20], [0, 10, 20]), ([0, 10, 20], [0, 30, 101])])
+def test_bad_borders_are_reported_and_nothing_is_written(cq, ck):
+    q, k, v, dout, _, _, _, _ = make([100], [100], 2, 1, 64)
+    dev = lambda c: torch.tensor(c, dtype=torch.int32, device="cuda")
+    ws = nabla.packed_workspace(q, k, 2)
+    o = torch.full(q.shape, 7.0, dtype=BF, device="cuda")
+    nabla.attn_packed_fwd(q, k, v, dev(cq), dev(ck), o=o, ws=ws)
+    assert nabla.status(ws) == nabla.ERR_PARAM
+    assert bool((o == 7).all())
+    nabla.attn_packed_fwd(q, k, v, dev([0, 50, 100]), dev([0, 50, 100]), o=o, ws=ws)
+    assert nabla.status(ws) == nabla.OK and not bool((o == 7).all())
+
+
+def test_stream_graph_and_many_sequences():
+    lens = [(i * 37) % 50 for i in range(1000)]
+    q, k, v, _, cq, ck, cu, _ = make(lens, lens, 2, 1, 64, seed=4)
+    want, _ = run_fwd(q, k, v, cu, cu, True)
+    some = 100
+    r = seq_util.packed(q, k, v, cq[:some], ck[:some], True)
+    seq_util.check(want, r["o"], r["o_tol"], "o")
+    ws = nabla.packed_workspace(q, k, 1000)
+    o = torch.zeros_like(want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        nabla.attn_packed_fwd(q, k, v, cu, cu, causal=True, o=o, ws=ws)
+    s.synchronize()
+    assert torch.equal(o, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nabla.attn_packed_fwd(q, k, v, cu, cu, causal=True, o=o, ws=ws)
+    o.zero_()
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and nabla.status(ws) == nabla.OK
