@@ -10,11 +10,13 @@
 #include "paged.cuh"
 #include "rope.cuh"
 
-// launchers (rope.cu, packed_fwd.cu, paged.cu)
+// launchers (rope.cu, packed_fwd.cu, packed_bwd.cu, paged.cu)
 cudaError_t nabla_launch_rope(nabla::RopeArgs &a, int dtype, int layout, int wide,
                               cudaStream_t stream);
 cudaError_t nabla_launch_packed_fwd(const nabla::packed::Args &a, int D, int64_t units, int splits,
                                     cudaStream_t stream);
+cudaError_t nabla_launch_packed_bwd(const nabla::packed::Args &a, int D, int64_t q_tiles,
+                                    int64_t row_tiles, int64_t key_tiles, cudaStream_t stream);
 cudaError_t nabla_launch_append(const nabla::AppendArgs &a, cudaStream_t stream);
 cudaError_t nabla_launch_paged(const nabla::PagedArgs &a, cudaStream_t stream);
 
@@ -368,6 +370,61 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
     a.lse = lse;
     a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kStatusBytes);
     return cuda_status(nabla_launch_packed_fwd(a, shape->D, units, fwd_splits(shape), s));
+}
+
+int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const nabla_view *k,
+                          const nabla_view *v, const nabla_view *o, const nabla_view *dout,
+                          const float *lse, const int32_t *cu_q, const int32_t *cu_k,
+                          const nabla_view *dq, const nabla_view *dk, const nabla_view *dv,
+                          void *workspace, size_t workspace_bytes, nabla_stream_t stream) {
+    int st = check_packed(shape, cu_q, cu_k, NABLA_PACKED_BWD, workspace, workspace_bytes);
+    if (st != NABLA_OK) return st;
+    const nabla_view *in[5] = {q, k, v, o, dout}, *out[3] = {dq, dk, dv};
+    Box bi[5], bo[3];
+    const bool of_q[5] = {true, false, false, true, true}, out_q[3] = {true, false, false};
+    auto view = [&](const nabla_view *x, bool is_q, bool written, Box *b) {
+        return packed_view(x, is_q ? shape->total_q : shape->total_k, is_q ? shape->heads : shape->heads_kv,
+                           shape->D, written, b);
+    };
+    for (int i = 0; i < 5; ++i)
+        if ((st = view(in[i], of_q[i], false, &bi[i])) != NABLA_OK) return st;
+    for (int i = 0; i < 3; ++i)
+        if ((st = view(out[i], out_q[i], true, &bo[i])) != NABLA_OK) return st;
+    if (shape->total_q > 0 && lse == nullptr) return NABLA_ERR_NULL;
+    // the three kernels read the inputs while the first outputs are written
+    for (int i = 0; i < 3; ++i) {
+        if ((out_q[i] ? shape->total_q : shape->total_k) == 0) continue;
+        for (int j = 0; j < 5; ++j)
+            if ((of_q[j] ? shape->total_q : shape->total_k) > 0 && !disjoint(bo[i], bi[j]))
+                return NABLA_ERR_PARAM;
+        for (int j = 0; j < i; ++j)
+            if ((out_q[j] ? shape->total_q : shape->total_k) > 0 && !disjoint(bo[i], bo[j]))
+                return NABLA_ERR_PARAM;
+    }
+    const int64_t G = shape->heads / shape->heads_kv;
+    const int64_t q_tiles = shape->total_q / 64 + shape->seqs;
+    const int64_t row_tiles = shape->total_q * G / 128 + shape->seqs;
+    const int64_t key_tiles = shape->total_k / 128 + shape->seqs;
+    if (row_tiles * shape->heads_kv > INT32_MAX || key_tiles * shape->heads_kv > INT32_MAX)
+        return NABLA_ERR_SHAPE;
+    cudaStream_t s = as_stream(stream);
+    if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return NABLA_ERR_CUDA;
+    if (shape->total_q == 0 && shape->total_k == 0) return NABLA_OK;
+    nabla::packed::Args a = packed_args(shape, cu_q, cu_k, workspace);
+    a.q = dev_view(q);
+    a.k = dev_view(k);
+    a.v = dev_view(v);
+    a.o = dev_view(o);
+    a.dout = dev_view(dout);
+    a.dq = dev_view(dq);
+    a.dk = dev_view(dk);
+    a.dv = dev_view(dv);
+    a.lse = const_cast<float *>(lse);
+    a.pad_rows = q_tiles * 64;
+    unsigned char *w = static_cast<unsigned char *>(workspace) + kStatusBytes;
+    a.pad_l = reinterpret_cast<float *>(w);
+    a.pad_d = reinterpret_cast<float *>(w + round256(sizeof(float) * a.pad_rows * shape->heads));
+    return cuda_status(nabla_launch_packed_bwd(a, shape->D, q_tiles, row_tiles, key_tiles, s));
 }
 
 int nabla_cache_append(const nabla_cache *cache, const nabla_view *k, const nabla_view *v,

@@ -25,7 +25,7 @@ SYMBOLS = ("nabla_flatten", "nabla_workspace_size", "nabla_mask_bytes", "nabla_b
            "nabla_build_mask_grid", "nabla_build_mask_static", "nabla_build_mask_dr",
            "nabla_attn_fwd", "nabla_attn_bwd", "nabla_status", "nabla_strerror",
            "nabla_rope", "nabla_packed_workspace_size", "nabla_attn_packed_fwd",
-           "nabla_cache_append", "nabla_paged_workspace_size",
+           "nabla_attn_packed_bwd", "nabla_cache_append", "nabla_paged_workspace_size",
            "nabla_attn_paged")
 DR_STATIC_RATIO, DR_THRESHOLD = 0, 1
 ROPE_ADJACENT, ROPE_HALVES = 0, 1
@@ -125,6 +125,8 @@ def lib():
         L.nabla_packed_workspace_size.restype = SZ
         L.nabla_attn_packed_fwd.argtypes = [P, P, P, P, P, P, P, P, P, SZ, P]
         L.nabla_attn_packed_fwd.restype = I
+        L.nabla_attn_packed_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
+        L.nabla_attn_packed_bwd.restype = I
         L.nabla_cache_append.argtypes = [P, P, P, I64, P, P, P, SZ, P]
         L.nabla_cache_append.restype = I
         L.nabla_paged_workspace_size.argtypes = [P, I]
@@ -476,6 +478,29 @@ def attn_packed_fwd(q, k, v, cu_q, cu_k, causal=False, scale=None, o=None, lse=N
                                            _ptr(cu_q), _ptr(cu_k), _tokens(o), _ptr(lse), _ptr(ws),
                                            ws.numel(), _stream(q)), "nabla_attn_packed_fwd")
     return o, lse
+
+
+def attn_packed_bwd(q, k, v, o, dout, lse, cu_q, cu_k, causal=False, scale=None, dq=None, dk=None,
+                    dv=None, ws=None):
+    """Gradients dq, dk, dv of attn_packed_fwd from its o and lse."""
+    s = _packed_of(q, k, v, cu_q, cu_k, causal, scale)
+    for t, n in ((o, "o"), (dout, "dout")):
+        _same(_rows(t, 3, torch.bfloat16, n, q), q.shape, n)
+    _need(lse, torch.float32, "lse")
+    _same(lse, (q.shape[1], q.shape[0]), "lse")
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+    for t, like, n in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        _same(_rows(t, 3, torch.bfloat16, n, q), like.shape, n)
+    ws = packed_workspace(q, k, s.seqs, back=True) if ws is None else _work(ws, q)
+    with _on(q):
+        _check(lib().nabla_attn_packed_bwd(ctypes.byref(s), _tokens(q), _tokens(k), _tokens(v),
+                                           _tokens(o), _tokens(dout), _ptr(lse), _ptr(cu_q),
+                                           _ptr(cu_k), _tokens(dq), _tokens(dk), _tokens(dv),
+                                           _ptr(ws), ws.numel(), _stream(q)),
+               "nabla_attn_packed_bwd")
+    return dq, dk, dv
 
 
 def _cache_of(k_cache, v_cache, table, seqs):

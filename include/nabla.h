@@ -376,6 +376,15 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
                           const nabla_view *o, float *lse, void *workspace, size_t workspace_bytes,
                           nabla_stream_t stream);
 
+/* Gradients of nabla_attn_packed_fwd from its o and lse (formulas as
+ * nabla_attn_bwd; dk and dv summed over the query heads of a key head).
+ * Deterministic, no atomics. */
+int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const nabla_view *k,
+                          const nabla_view *v, const nabla_view *o, const nabla_view *dout,
+                          const float *lse, const int32_t *cu_q, const int32_t *cu_k,
+                          const nabla_view *dq, const nabla_view *dk, const nabla_view *dv,
+                          void *workspace, size_t workspace_bytes, nabla_stream_t stream);
+
 /* A paged key-value cache: k and v are pools of `pages` pages of page_size
  * rows, heads_kv heads and D features (bf16; batch = distance between pages).
  * Row p of sequence s is row p % page_size of page

@@ -185,3 +185,28 @@ def test_binding_refuses_what_it_is_not_given():
         nabla.attn_packed_fwd(x, x, x, cu, cu)
     with pytest.raises(ValueError):
         nabla.attn_paged(x, x[None], x[None], cu[None], cu)
+
+
+def test_packed_backward_rejects_on_host(L):
+    far = 1 << 30
+    names = ("q", "k", "v", "o", "dout", "dq", "dk", "dv")
+
+    def call(s=None, lse=BASE, ws=BASE, ws_bytes=1 << 40, **v):
+        s = packed() if s is None else s
+        d = {n: view(BASE + (i + 1) * far, token=1024) for i, n in enumerate(names)}
+        d.update(v)
+        r = lambda n: None if d[n] is None else ctypes.byref(d[n])
+        return L.nabla_attn_packed_bwd(ctypes.byref(s), *(r(n) for n in names[:5]), lse, BASE, BASE,
+                                       *(r(n) for n in names[5:]), ws, ws_bytes, None)
+    assert call(packed(D=32)) == nabla.ERR_SHAPE
+    assert call(packed(scale=-1.0)) == nabla.ERR_PARAM
+    for n in names:
+        assert call(**{n: None}) == nabla.ERR_NULL
+        assert call(**{n: view(BASE + 20 * far + 4, 1024)}) == nabla.ERR_ALIGN
+    assert call(lse=None) == nabla.ERR_NULL
+    assert call(ws_bytes=256) == nabla.ERR_WORKSPACE
+    assert call(dq=view(BASE + far, 1024)) == nabla.ERR_PARAM         # dq is q
+    assert call(dk=view(BASE + 8 * far, 1024)) == nabla.ERR_PARAM     # dk is dv
+    assert call(dv=view(BASE + 20 * far, 64)) == nabla.ERR_PARAM      # rows of dv overlap
+    size = lambda op: L.nabla_packed_workspace_size(ctypes.byref(packed()), op)
+    assert size(nabla.PACKED_BWD) == 256 + 2 * ((4 * (1000 // 64 + 3) * 64 * 8 + 255) // 256 * 256)

@@ -174,3 +174,112 @@ def test_stream_graph_and_many_sequences():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, want) and nabla.status(ws) == nabla.OK
+
+
+# ---------------------------------------------------------------------------
+# backward
+# ---------------------------------------------------------------------------
+def run_both(q, k, v, dout, cu_q, cu_k, causal, **kw):
+    ws = nabla.packed_workspace(q, k, cu_q.numel() - 1, back=True)
+    o, lse = nabla.attn_packed_fwd(q, k, v, cu_q, cu_k, causal=causal, ws=ws, **kw)
+    assert nabla.status(ws) == nabla.OK
+    full = lambda t: torch.full(t.shape, 7.0, dtype=BF, device="cuda")
+    dq, dk, dv = full(q), full(k), full(v)
+    nabla.attn_packed_bwd(q, k, v, o, dout, lse, cu_q, cu_k, causal=causal, dq=dq, dk=dk, dv=dv, ws=ws,
+                          **kw)
+    assert nabla.status(ws) == nabla.OK
+    return dq, dk, dv
+
+
+def check_grads(got, r, n, m):
+    for name, g, rows in zip(("dq", "dk", "dv"), got, (n, m, m)):
+        assert bool((g[rows:] == 7).all()), name  # rows of no sequence
+        seq_util.check(g[:rows], r[name][:rows], r[name + "_tol"][:rows], name)
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D", [128, 64])
+def test_backward(case, causal, D):
+    lens_q, lens_k, hq, hk = CASES[case]
+    q, k, v, dout, cq, ck, cu_q, cu_k = make(lens_q, lens_k, hq, hk, D, seed=case, behind=70)
+    got = run_both(q, k, v, dout, cu_q, cu_k, causal)
+    r = seq_util.packed(q, k, v, cq, ck, causal, dout=dout)
+    check_grads(got, r, cq[-1], ck[-1])
+
+
+def test_backward_neighbours_strides_and_repeatability():
+    """NaN in the sequences around one; slices of a fused projection, gradients
+    into slices of another; the same bits every time."""
+    L, hq, hk, D = 400, 6, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(2)
+    qkv = torch.randn(L, hq + 2 * hk, D, generator=g, device="cuda").to(BF)
+    dout = torch.randn(L, hq, D, generator=g, device="cuda").to(BF)
+    for t in (qkv, dout):
+        t[:10], t[10:100], t[230:] = math.nan, math.inf, math.nan
+    cu = torch.tensor([10, 100, 230, 390], dtype=torch.int32, device="cuda")
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    for causal in (False, True):
+        ws = nabla.packed_workspace(q, k, 3, back=True)
+        o, lse = nabla.attn_packed_fwd(q, k, v, cu, cu, causal=causal, ws=ws)
+        out = []
+        for _ in range(2):
+            d = torch.full(qkv.shape, 7.0, dtype=BF, device="cuda")
+            dq, dk, dv = d[:, :hq], d[:, hq:hq + hk], d[:, hq + hk:]
+            nabla.attn_packed_bwd(q, k, v, o, dout, lse, cu, cu, causal=causal, dq=dq, dk=dk, dv=dv, ws=ws)
+            out.append(d)
+        r = seq_util.packed(q, k, v, [100, 230], [100, 230], causal, dout=dout)
+        for n, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+            seq_util.check(t[100:230], r[n][100:230], r[n + "_tol"][100:230], n)
+        assert torch.equal(out[0][100:230], out[1][100:230])
+        assert bool((d[:10] == 7).all()) and bool((d[390:] == 7).all())
+
+
+def test_gradients_against_differences():
+    """Central differences of the float64 loss sum(o dout) along single
+    coordinates: error of the differences ~ eps^2 |f'''| + 2^-52 |f| / eps."""
+    lens_q, lens_k, hq, hk, D = [70, 33], [70, 50], 4, 2, 64
+    q, k, v, dout, cq, ck, cu_q, cu_k = make(lens_q, lens_k, hq, hk, D, seed=11)
+    got = run_both(q, k, v, dout, cu_q, cu_k, True)
+    r = seq_util.packed(q, k, v, cq, ck, True, dout=dout)
+    base = {"q": q.double(), "k": k.double(), "v": v.double()}
+
+    def loss(p):
+        return float((seq_util.packed(p["q"], p["k"], p["v"], cq, ck, True)["o"] * dout.double()).sum())
+    eps = 1e-4
+    for i, name in enumerate(("q", "k", "v")):
+        for at in ((0, 0, 0), (69, 1, 63), (75, 1, 17), (30, 0, 40)):
+            p = {n: t.clone() for n, t in base.items()}
+            p[name][at] += eps
+            up = loss(p)
+            p[name][at] -= 2 * eps
+            diff = (up - loss(p)) / (2 * eps)
+            tol = float(r["d" + name + "_tol"][at]) + 1e-5
+            assert abs(float(got[i][at]) - diff) <= tol, (name, at)
+
+
+def test_backward_in_a_graph_and_zero_rows():
+    q, k, v, dout, cq, ck, cu_q, cu_k = make([100, 40], [100, 40], 4, 2, 128, seed=1)
+    want = run_both(q, k, v, dout, cu_q, cu_k, True)
+    ws = nabla.packed_workspace(q, k, 2, back=True)
+    o, lse = torch.empty_like(q), torch.empty(4, 140, device="cuda")
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nabla.attn_packed_fwd(q, k, v, cu_q, cu_k, causal=True, o=o, lse=lse, ws=ws)
+        nabla.attn_packed_bwd(q, k, v, o, dout, lse, cu_q, cu_k, causal=True, dq=grads[0], dk=grads[1],
+                              dv=grads[2], ws=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))
+    # no query at all: dk = dv = 0; no key at all: o = 0, dq = 0
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")
+    e = q[:0]
+    o0, lse0 = nabla.attn_packed_fwd(e, k, v, none, cu_k)
+    _, dk, dv = nabla.attn_packed_bwd(e, k, v, o0, e, lse0, none, cu_k)
+    assert bool((dk == 0).all()) and bool((dv == 0).all())
+    o1, lse1 = nabla.attn_packed_fwd(q, k[:0], v[:0], cu_q, none)
+    assert bool((o1 == 0).all()) and bool((lse1 == -math.inf).all())
+    dq, _, _ = nabla.attn_packed_bwd(q, k[:0], v[:0], o1, dout, lse1, cu_q, none)
+    assert bool((dq == 0).all())
