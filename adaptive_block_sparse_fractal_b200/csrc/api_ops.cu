@@ -13,7 +13,7 @@
 // launchers (rope.cu, packed_fwd.cu, packed_bwd.cu, paged.cu)
 cudaError_t nabla_launch_rope(nabla::RopeArgs &a, int dtype, int layout, int wide,
                               cudaStream_t stream);
-cudaError_t nabla_launch_packed_fwd(const nabla::packed::Args &a, int D, int64_t units, int splits,
+cudaError_t nabla_launch_packed_fwd(const nabla::packed::Args &a, int D, int64_t units,
                                     cudaStream_t stream);
 cudaError_t nabla_launch_packed_bwd(const nabla::packed::Args &a, int D, int64_t q_tiles,
                                     int64_t row_tiles, int64_t key_tiles, cudaStream_t stream);
@@ -115,15 +115,17 @@ constexpr int64_t kMaxPackedRows = (1ll << 31) - 1024;
 
 bool packed_shape_ok(const nabla_packed *s) {
     return s->seqs >= 1 && s->heads >= 1 && s->heads_kv >= 1 && s->heads % s->heads_kv == 0 &&
-           (s->D == 64 || s->D == 128) && s->total_q >= 0 && s->total_k >= 0 &&
+           s->heads / s->heads_kv <= 128 && (s->D == 64 || s->D == 128) && s->total_q >= 0 && s->total_k >= 0 &&
            s->total_k <= kMaxPackedRows && s->total_q <= kMaxPackedRows / s->heads &&
            s->seqs <= (1 << 24);
 }
 
-// 256-row forward units of all key heads, at most (every sequence may end inside one)
+// Tokens of a row tile of the forward: 128 rows hold them for all heads of a group.
+int tile_tokens(const nabla_packed *s) { return 128 / (s->heads / s->heads_kv); }
+
+// Forward units (two row tiles) of all key heads, at most: every sequence may end inside one.
 int64_t fwd_units(const nabla_packed *s) {
-    const int64_t G = s->heads / s->heads_kv;
-    return (s->total_q * G / 256 + s->seqs) * s->heads_kv;
+    return (s->total_q / (2 * tile_tokens(s)) + s->seqs) * s->heads_kv;
 }
 
 // Splits of the key range.  One CTA walks 128 keys in about a microsecond, so
@@ -194,6 +196,8 @@ nabla::packed::Args packed_args(const nabla_packed *s, const int32_t *cu_q, cons
     a.heads_kv = s->heads_kv;
     a.group = s->heads / s->heads_kv;
     a.causal = s->causal;
+    a.tile_tokens = tile_tokens(s);
+    a.splits = 1;
     a.c = s->scale * 1.4426950408889634f;
     a.scale = s->scale;
     a.limit = 1000000000u;  // 1 s per wait
@@ -358,9 +362,11 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
                                                      (!disjoint(bo, bk) || !disjoint(bo, bv)))))
         return NABLA_ERR_PARAM;
     const int64_t units = fwd_units(shape);
-    if (units > INT32_MAX) return NABLA_ERR_SHAPE;
+    const int splits = fwd_splits(shape);
+    if (units > INT32_MAX / splits) return NABLA_ERR_SHAPE;
     cudaStream_t s = as_stream(stream);
-    if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return NABLA_ERR_CUDA;
+    // the status word and the unit counter behind it
+    if (cudaMemsetAsync(workspace, 0, 2 * sizeof(int), s) != cudaSuccess) return NABLA_ERR_CUDA;
     if (shape->total_q == 0) return NABLA_OK;
     nabla::packed::Args a = packed_args(shape, cu_q, cu_k, workspace);
     a.q = dev_view(q);
@@ -369,7 +375,8 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
     a.o = dev_view(o);
     a.lse = lse;
     a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kStatusBytes);
-    return cuda_status(nabla_launch_packed_fwd(a, shape->D, units, fwd_splits(shape), s));
+    a.splits = splits;
+    return cuda_status(nabla_launch_packed_fwd(a, shape->D, units * splits, s));
 }
 
 int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const nabla_view *k,

@@ -20,11 +20,12 @@ struct Args {
     View q, k, v, o, dout, dq, dk, dv;
     const int32_t *cu_q, *cu_k;
     float *lse;        // [heads, total_q]
-    int *status;       // workspace status word
+    int *status;       // workspace status word; behind it the forward's unit counter
     float *pad_l, *pad_d;  // backward: [heads, pad_rows], -lse log2(e) and -dout.o
     float *part;       // split forward: partial rows, then their (m, l)
     int64_t total_q, total_k, pad_rows;
     int seqs, heads, heads_kv, group, causal;
+    int tile_tokens, splits;  // forward: tokens a row tile (128 / group), splits of the key range
     float c, scale;    // scale * log2(e), scale
     uint32_t limit;    // ns per wait
 };
@@ -95,6 +96,69 @@ __device__ __forceinline__ bool find_seq(const Args &a, int64_t unit, Count coun
     return out->seq >= 0;
 }
 
+constexpr int kSms = 148;  // CTAs of a persistent launch
+
+// Every thread of the CTA looks at some borders; see find_seq.
+__device__ __forceinline__ bool borders_ok(const Args &a) {
+    bool good = true;
+    for (int s = threadIdx.x; s < a.seqs; s += blockDim.x) {
+        const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
+        good = good && q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k;
+    }
+    return good;
+}
+
+// The next unit of a persistent launch (the counter starts at 0; the order in
+// which CTAs take units does not change what a unit computes).
+__device__ __forceinline__ int64_t take_unit(const Args &a) {
+    return static_cast<int64_t>(atomicAdd(reinterpret_cast<unsigned int *>(a.status) + 1, 1u));
+}
+
+// One warp's walk over the sequences for units that only grow: 32 sequences at
+// a time, their borders and running tile counts in registers.
+struct UnitScan {
+    int base, q0, q1, k0, k1;
+    int64_t front, all;  // tiles in front of this lane's sequence and of the next 32
+    __device__ __forceinline__ UnitScan() : base(-32), q0(0), q1(0), k0(0), k1(0), front(0), all(0) {}
+    // sequence and tile (of `tile` tokens) of unit x; false behind the last
+    __device__ __forceinline__ bool find(const Args &a, int64_t x, int tile_len, int lane, int *oq0,
+                                         int *oLq, int *ok0, int *oLk, int *tile) {
+        while (x >= all) {
+            base += 32;
+            if (base >= a.seqs) {
+                base -= 32;
+                return false;
+            }
+            const int s = base + lane;
+            q0 = q1 = k0 = k1 = 0;
+            if (s < a.seqs) {
+                q0 = a.cu_q[s];
+                q1 = a.cu_q[s + 1];
+                k0 = a.cu_k[s];
+                k1 = a.cu_k[s + 1];
+            }
+            int64_t incl = (q1 - q0 + tile_len - 1) / tile_len;
+            const int64_t mine = incl;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += t;
+            }
+            front = all + incl - mine;
+            all += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        // the last lane whose sequence starts at or before x (empty ones share a start)
+        const uint32_t at = __ballot_sync(0xffffffffu, front <= x);
+        const int src = 31 - __clz(at);
+        *oq0 = __shfl_sync(0xffffffffu, q0, src);
+        *oLq = __shfl_sync(0xffffffffu, q1, src) - *oq0;
+        *ok0 = __shfl_sync(0xffffffffu, k0, src);
+        *oLk = __shfl_sync(0xffffffffu, k1, src) - *ok0;
+        *tile = static_cast<int>(x - __shfl_sync(0xffffffffu, front, src));
+        return true;
+    }
+};
+
 // box of 64 features x one head x `rows` tokens
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint64_t *bar,
                                             int x, int y, int z) {
@@ -103,6 +167,30 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         "[%0], [%1, {%3, %4, %5}], [%2];\n" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
         : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit TMEM columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *v) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// tcgen05.wait::ld that the 32 values of a load pass through, so that their
+// uses stay behind it while other loads or arithmetic are in flight.
+__device__ __forceinline__ void tmem_wait_ld_of(float *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                 :
+                 : "memory");
 }
 
 // Register share of a warpgroup (all four of its warps execute it).
@@ -130,7 +218,7 @@ __device__ __forceinline__ void zero_rows(unsigned char *tile, int from, int row
 }  // namespace packed
 }  // namespace nabla
 
-// Host: tensor map over a [tokens, heads, D] bf16 view, boxes of 64 features of
-// one head x `rows` tokens, 128-byte swizzle (defined in packed_fwd.cu).
+// Host: tensor map over a [tokens, heads, D] bf16 view, boxes of 64 features x
+// box_heads heads x `rows` tokens, 128-byte swizzle (defined in packed_fwd.cu).
 bool nabla_make_tmap_view(CUtensorMap *m, const nabla::packed::View &v, int64_t tokens, int heads,
-                          int D, int rows);
+                          int D, int rows, int box_heads);

@@ -712,11 +712,11 @@ static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_til
     const bool q = a.total_q > 0, k = a.total_k > 0;
     const View &any = q ? a.q : a.k;
     CUtensorMap mq, mdo, mk, mv, mv128;
-    if (!nabla_make_tmap_view(&mq, q ? a.q : any, q ? a.total_q : 1, q ? a.heads : 1, D, 64) ||
-        !nabla_make_tmap_view(&mdo, q ? a.dout : any, q ? a.total_q : 1, q ? a.heads : 1, D, 64) ||
-        !nabla_make_tmap_view(&mk, k ? a.k : any, k ? a.total_k : 1, k ? a.heads_kv : 1, D, 64) ||
-        !nabla_make_tmap_view(&mv, k ? a.v : any, k ? a.total_k : 1, k ? a.heads_kv : 1, D, 64) ||
-        !nabla_make_tmap_view(&mv128, k ? a.v : any, k ? a.total_k : 1, k ? a.heads_kv : 1, D, 128))
+    if (!nabla_make_tmap_view(&mq, q ? a.q : any, q ? a.total_q : 1, q ? a.heads : 1, D, 64, 1) ||
+        !nabla_make_tmap_view(&mdo, q ? a.dout : any, q ? a.total_q : 1, q ? a.heads : 1, D, 64, 1) ||
+        !nabla_make_tmap_view(&mk, k ? a.k : any, k ? a.total_k : 1, k ? a.heads_kv : 1, D, 64, 1) ||
+        !nabla_make_tmap_view(&mv, k ? a.v : any, k ? a.total_k : 1, k ? a.heads_kv : 1, D, 64, 1) ||
+        !nabla_make_tmap_view(&mv128, k ? a.v : any, k ? a.total_k : 1, k ? a.heads_kv : 1, D, 128, 1))
         return cudaErrorInvalidValue;
     if (k) {
         constexpr uint32_t kSmem = KvLayout<D>::kSmem;
