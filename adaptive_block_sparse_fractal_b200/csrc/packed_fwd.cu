@@ -10,8 +10,8 @@
 //
 // Per 128-key tile and row tile t:
 //   S_t = Q_t . K^T    (both from shared memory, accumulator in TMEM)
-//   P_t = exp2(S_t scale log2e - m)   one softmax warpgroup per row tile, one
-//                      thread per row: no exchange between threads at all
+//   P_t = exp2(S_t scale log2e - m)   two softmax warpgroups per row tile:
+//                      thread (h, r) takes row r and keys [64 h, +64)
 //   O_t += P_t . V     (P_t in TMEM over S_t, V from shared memory)
 // The tensor core works for one row tile while the other is in its softmax.
 //
@@ -22,11 +22,13 @@
 // [-1/2, 1/2] (2.6e-6, found with a Remez iteration; P is rounded to bf16, at
 // 2e-3, next).
 //
-// A row's reference is the maximum of its first tile.  Later tiles are taken
-// against it without looking for their own maximum: P (bf16) and the float32
-// sums have the exponent range for it.  Only when a tile's sum passes 2^16 is it
-// taken again, against its true maximum, to which O (in TMEM) and the sum
-// then move.  That leaves the loop with five instructions a pair of scores.
+// A row's reference is the maximum of its first tile (and of masked ones).
+// Other tiles are taken against it without looking for their own maximum: P
+// (bf16) and the float32 accumulators have the exponent range for scores far
+// above it.  That leaves five instructions a pair of scores in the loop, no
+// exchange between threads, and P goes over to the tensor core in two parts as
+// it is made.  A unit in which some tile's sum passed 2^60 (or is NaN) is not
+// written but taken once more, moving to the true maximum at every tile.
 // Statistics and sums are float32; P is rounded to bf16 (half a step, 2^-8
 // relative) because it is the tensor core's operand, the sum of a row is taken
 // over the float32 values in front of that rounding.
@@ -44,15 +46,18 @@
 // Few rows against many keys (new tokens behind a cached context) leave the
 // SMs idle: the key range is then split and combine_kernel joins the parts.
 //
-// Warp roles (384 threads): warp 0 takes units and loads by TMA, warps 1 and 2
-// issue the MMAs of row tiles 0 and 1, warps 4-7 and 8-11 are their softmax
-// (warp 3 only completes the first warpgroup).  The issuing warps stay converged
+// Warp roles (640 threads): warp 0 takes units and loads by TMA, warps 1 and 2
+// issue the MMAs of row tiles 0 and 1, warps 4-11 and 12-19 are their softmax
+// (warp 3 only completes the first warpgroup).  With one thread per row of 128
+// scores there was one softmax warp of a tile on each scheduler, and its
+// latencies, not its pipes, set the pace (1,450 cycles a tile).  The issuing warps stay converged
 // and send four MMAs per elect.sync (a lone lane takes about as long to issue an
 // MMA as it runs).  They take turns, PV_0 S_0 then PV_1 S_1, each waiting for its
 // operands before its turn: the MMAs of a turn go out in one run, and the row
 // tiles stay half a period apart (free-running issuers fell into step, both
 // in their softmax and then both at the tensor core, and lost 15%).
-// TMEM columns: S_0 [0,128), S_1 [128,256), O_0 [256, +D), O_1 [384, +D).
+// TMEM columns: S_0 [0,128), S_1 [128,256), O_0 [256, +D), O_1 [384, +D); the
+// bf16 P of keys [64 h, +64) takes the first 32 columns of their scores.
 #include "packed.cuh"
 
 namespace nabla {
@@ -60,19 +65,21 @@ namespace packed {
 
 using namespace sm100;
 
-constexpr int kFwdThreads = 384;
-// Registers a thread: the launch gives 168 to each of the three warpgroups; the
-// first (loads, MMA issue) hands some over to the softmax ones, whose rows of
-// 128 scores need them: 80 + 2 * 208 = 496 <= 3 * 168.
-constexpr int kRegsFew = 80, kRegsMany = 208;
+constexpr int kFwdThreads = 640;
+// Registers a thread: the launch gives 96 to each of the five warpgroups; the
+// first (loads, MMA issue) hands some over to the four softmax ones:
+// 64 + 4 * 104 = 480 = 5 * 96.
+constexpr int kRegsFew = 64, kRegsMany = 104;
 constexpr int kTileKeys = 128;
 constexpr float kFwdLn2 = 0.6931471805599453f;
-constexpr float kMaxSum = 65536.f;  // largest sum of a row's P over a tile against an old reference
-constexpr int kPolyOf8 = 3;       // pairs of every 8 whose exponentials the FMA pipe takes
+constexpr float kMaxSum = 1152921504606846976.f;  // 2^60: largest sum of P over a tile's half row
+constexpr int kPolyOf8 = 2;       // pairs of every 8 whose exponentials the FMA pipe takes
 
 // One unit, as the loading warp hands it to the others.
 struct Unit {
     int valid, hk, split;
+    int exact;    // every tile moves to its true maximum
+    int redo;     // set by the softmax: to be taken again, exactly
     int q0, Lq, k0, Lk;
     int tok0;     // first token of row tile 0
     int j0;       // first key tile of this split
@@ -87,46 +94,56 @@ struct FwdLayout {
     static constexpr uint32_t OFF_Q = 0;             // two row tiles
     static constexpr uint32_t OFF_RING = 2 * kTile;
     static constexpr uint32_t OFF_BAR = OFF_RING + kRing * kTile;
-    static constexpr int kBars = 2 * kRing + 4 + 2 + 2 + 2 + 4 + 1 + 4;
+    static constexpr int kBars = 2 * kRing + 4 + 2 + 4 + 2 + 4 + 1 + 4;
     static constexpr uint32_t OFF_UNIT = OFF_BAR + 8 * kBars;
-    static constexpr uint32_t OFF_INT = OFF_UNIT + 2 * sizeof(Unit);
-    static constexpr uint32_t kSmem = OFF_INT + 16 + 1024;
+    static constexpr uint32_t OFF_RED = (OFF_UNIT + 2 * sizeof(Unit) + 15) / 16 * 16;  // maxima or sums: [tile][half][row]
+    static constexpr uint32_t OFF_INT = OFF_RED + 2 * 2 * 128 * 4;
+    static constexpr uint32_t kSmem = OFF_INT + 16;  // no room for an alignment pad at D = 128
 };
 
-// 2^x for both halves of a pair, x finite and <= about 2^8, on the FMA pipe
-__device__ __forceinline__ void exp2_poly(uint64_t x, float &p0, float &p1) {
+// 2^x of a pair on the SFU
+__device__ __forceinline__ uint64_t exp2_sfu(uint64_t x) {
+    uint64_t y;
+    asm("{\n .reg .f32 a, b;\n mov.b64 {a, b}, %1;\n ex2.approx.ftz.f32 a, a;\n ex2.approx.ftz.f32 b, b;\n"
+        " mov.b64 %0, {a, b};\n}\n"
+        : "=l"(y)
+        : "l"(x));
+    return y;
+}
+// 2^x of a pair, x <= about 2^7, on the FMA pipe
+__device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
     constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-    const uint64_t big = f2_pack(kRound, kRound), nbig = f2_pack(-kRound, -kRound);
     x = f2_pack(fmaxf(f2_lo(x), -126.f), fmaxf(f2_hi(x), -126.f));
-    const uint64_t t = f2_add(x, big);
-    const uint64_t f = f2_fma(f2_add(t, nbig), f2_pack(-1.f, -1.f), x);
+    const uint64_t t = f2_add(x, f2_pack(kRound, kRound));
+    const uint64_t f = f2_fma(f2_add(t, f2_pack(-kRound, -kRound)), f2_pack(-1.f, -1.f), x);
     uint64_t p = f2_fma(f2_pack(0.009570101911165427f, 0.009570101911165427f), f,
                         f2_pack(0.055917860319388245f, 0.055917860319388245f));
     p = f2_fma(p, f, f2_pack(0.2402474482786378f, 0.2402474482786378f));
     p = f2_fma(p, f, f2_pack(0.6931218147366892f, 0.6931218147366892f));
     p = f2_fma(p, f, f2_pack(0.9999992614457122f, 0.9999992614457122f));
     // the integer stands in the low bits of t: into the exponent
-    p0 = __uint_as_float(static_cast<uint32_t>(p) + (static_cast<uint32_t>(t) << 23));
-    p1 = __uint_as_float(static_cast<uint32_t>(p >> 32) + (static_cast<uint32_t>(t >> 32) << 23));
+    const uint32_t lo = static_cast<uint32_t>(p) + (static_cast<uint32_t>(t) << 23);
+    const uint32_t hi = static_cast<uint32_t>(p >> 32) + (static_cast<uint32_t>(t >> 32) << 23);
+    return f2_pack(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint32_t pack_bf16_pair(uint64_t p) {
+    uint32_t d;
+    asm("{\n .reg .f32 a, b;\n mov.b64 {a, b}, %1;\n cvt.rn.bf16x2.f32 %0, b, a;\n}\n" : "=r"(d) : "l"(p));
+    return d;
 }
 
-// P of 32 keys from their scores, as packed bf16; adds the values to four sums.
+// P of 32 keys from their scores, as packed bf16; adds the values to two pairs of sums.
 template <int kPoly>
 __device__ __forceinline__ void softmax_part(const float *s, uint64_t c2, uint64_t nm2,
                                              uint64_t *ls2, uint32_t *pk) {
 #pragma unroll
     for (int k = 0; k < 32; k += 2) {
         const uint64_t x = f2_fma(f2_pack(s[k], s[k + 1]), c2, nm2);
-        float p0, p1;
-        // spread over the row, so that both pipes are busy at once
-        if (((k >> 1) * kPoly) % 8 + kPoly > 7 && kPoly > 0) {
-            exp2_poly(x, p0, p1);
-        } else {
-            p0 = fast_exp2(f2_lo(x));
-            p1 = fast_exp2(f2_hi(x));
-        }
-        ls2[(k >> 1) & 3] = f2_add(ls2[(k >> 1) & 3], f2_pack(p0, p1));
-        pk[k >> 1] = pack_bf16(p0, p1);
+        // the polynomial's pairs are spread over the row, so that both pipes are busy at once
+        const bool poly = ((k >> 1) * kPoly) % 8 + kPoly > 7 && kPoly > 0;
+        const uint64_t p = poly ? exp2_poly(x) : exp2_sfu(x);
+        ls2[(k >> 1) & 1] = f2_add(ls2[(k >> 1) & 1], p);
+        pk[k >> 1] = pack_bf16_pair(p);
     }
 }
 
@@ -137,17 +154,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     using L = FwdLayout<D>;
     constexpr int kRing = L::kRing, kHalves = L::kHalves;
     constexpr uint32_t kTile = L::kTile;
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw);
-    const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
-    unsigned char *sm = smem_raw + pad;
-    const uint32_t sb = raw + pad;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const uint32_t sb = smem_addr(sm);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::OFF_BAR);
     uint64_t *kv_full = bar, *kv_empty = bar + kRing;
     uint64_t *q_full = bar + 2 * kRing, *q_empty = q_full + 2;  // per row tile
-    // per row tile: S complete; P written (its four warps); PV complete
-    uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2;
-    // per unit slot: written by the loading warp; read by the ten others
+    // per row tile: S complete; the two parts of P written (its eight warps); PV complete
+    uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 4;
+    // per unit slot: written by the loading warp; read by the 18 others
     uint64_t *u_full = pv_done + 2, *u_empty = u_full + 2;
     uint64_t *raw_full = u_empty + 2;  // a tile that still has rows to zero
     uint64_t *all_done = raw_full + 1, *turn = all_done + 2;  // per issuing warp
@@ -168,10 +182,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(&all_done[t], 1);
             mbar_init(&turn[t], 1);
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], 4);
+            mbar_init(&p_full[2 * t], 8);
+            mbar_init(&p_full[2 * t + 1], 8);
             mbar_init(&pv_done[t], 1);
             mbar_init(&u_full[t], 1);
-            mbar_init(&u_empty[t], 10);
+            mbar_init(&u_empty[t], 18);
         }
         mbar_init(raw_full, 1);
         sInt[2] = *reinterpret_cast<volatile int *>(a.status) != 0 ? 1 : 0;
@@ -182,7 +197,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tmem_relinquish();
     }
     // every CTA looks at every border before anything is written
-    const bool good = borders_ok(a);
+    const bool good = borders_ok(a) && (sb & 1023u) == 0;  // (swizzled tiles need the alignment asked for above)
     tc_fence_before();
     const bool go = !__syncthreads_or(!good);
     tc_fence_after();
@@ -228,20 +243,48 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             };
             UnitScan scan;
             int64_t x = lane == 0 ? take_unit(a) : 0;
+            bool more = true;
+            int ends = 0;
             for (uint32_t n = 0; ok; ++n) {
-                x = __shfl_sync(0xffffffffu, x, 0);
-                const int64_t now = x;
-                if (lane == 0) x = take_unit(a);  // the next one, under this one's loads
+                // the slot's last unit is finished: it may have to be taken again
+                const int us = n & 1;
+                ok = __all_sync(0xffffffffu, lane != 0 || wait_bar(&u_empty[us], ((n >> 1) & 1u) ^ 1u, abort_flag,
+                                                                   a.status, a.limit));
+                if (!ok) break;
                 Unit u = {};
-                const int64_t ux = now / a.splits;
-                int tile;
-                u.split = static_cast<int>(now % a.splits);
-                u.hk = static_cast<int>(ux % a.heads_kv);
-                u.valid = scan.find(a, ux / a.heads_kv, 2 * tpt, lane, &u.q0, &u.Lq, &u.k0, &u.Lk, &tile);
-                int emax = 0;
-                if (u.valid) {
+                const bool again = n >= 2 && units[us].redo != 0;
+                if (again) {
+                    u.valid = 1;
+                    u.exact = 1;
+                    u.hk = units[us].hk;
+                    u.split = units[us].split;
+                    u.q0 = units[us].q0;
+                    u.Lq = units[us].Lq;
+                    u.k0 = units[us].k0;
+                    u.Lk = units[us].Lk;
+                    u.tok0 = units[us].tok0;
+                    u.j0 = units[us].j0;
+                    u.e[0] = units[us].e[0];
+                    u.e[1] = units[us].e[1];
+                } else if (more) {
+                    x = __shfl_sync(0xffffffffu, x, 0);
+                    const int64_t now = x;
+                    if (lane == 0) x = take_unit(a);  // the next one, under this one's loads
+                    const int64_t ux = now / a.splits;
+                    int tile = 0;
+                    u.split = static_cast<int>(now % a.splits);
+                    u.hk = static_cast<int>(ux % a.heads_kv);
+                    more = scan.find(a, ux / a.heads_kv, 2 * tpt, lane, &u.q0, &u.Lq, &u.k0, &u.Lk, &tile);
+                    u.valid = more ? 1 : 0;
                     // the last tiles of a causal sequence keep the most keys: they go first
                     u.tok0 = ((u.Lq + 2 * tpt - 1) / (2 * tpt) - 1 - tile) * 2 * tpt;
+                }
+                // behind the last unit: an empty one for each slot, in case the other
+                // slot's has to be taken again, then the end
+                const bool idle = !u.valid && ++ends <= 2;
+                if (!u.valid) u = {};  // no rows, no keys
+                if (idle) u.valid = 1;
+                if (u.valid && !again && !idle) {
                     const int off = u.Lk - u.Lq;
                     int kt[2];
 #pragma unroll
@@ -256,15 +299,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const int j1 = min(all, u.j0 + per);
                     u.e[0] = max(0, min(j1, kt[0]) - u.j0);
                     u.e[1] = max(0, min(j1, kt[1]) - u.j0);
-                    emax = max(u.e[0], u.e[1]);
                 }
-                const int us = n & 1;
-                ok = __all_sync(0xffffffffu, lane != 0 || wait_bar(&u_empty[us], ((n >> 1) & 1u) ^ 1u, abort_flag,
-                                                                   a.status, a.limit));
-                if (!ok) break;
+                if (again) ends = 0;
+                const int emax = max(u.e[0], u.e[1]);
+                __syncwarp();
                 if (lane == 0) {
                     volatile Unit &w = units[us];
                     w.valid = u.valid;
+                    w.exact = u.exact;
+                    w.redo = 0;
                     w.hk = u.hk;
                     w.split = u.split;
                     w.q0 = u.q0;
@@ -359,8 +402,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (lane == 0) mbar_arrive(&u_empty[us]);
                 if (!valid) break;
                 if (emax == 0) continue;
-                // turn -1: S(0); turn i: PV(i), S(i + 1).  All waits of a turn
-                // stand in front of it, so that its MMAs go out in one run.
+                // turn -1: S(0); turn i: PV(i), S(i + 1).  The waits of a turn stand in
+                // front of it, but for the second part of P, made under the first's MMAs.
                 if (e > 0) {
                     ok = warp_wait(&q_full[t], nq & 1u, abort_flag, a.status, a.limit);
                     ++nq;
@@ -384,23 +427,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const uint32_t vslot = slot;
                     next();
                     if (ok && more) ok = arrived();  // K(i + 1)
-                    if (ok && i < e) {
-                        ok = warp_wait(&p_full[t], np & 1u, abort_flag, a.status, a.limit);
-                        ++np;
-                    }
+                    if (ok && i < e) ok = warp_wait(&p_full[2 * t], np & 1u, abort_flag, a.status, a.limit);
                     ok = ok && my_turn();
                     if (!ok) break;
                     tc_fence_after();
                     if (i < e) {
                         const uint64_t vd = desc_sw128(sb + L::OFF_RING + vslot * kTile, 16384, 1024);
+                        // part p of P: keys [32 p, +32) and [64 + 32 p, +32); 16 keys are 8
+                        // columns of P and 2 KB of V
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            // 16 keys: 8 columns of P, 2 KB of V
-                            const uint32_t p = ds + 32 * half;
-                            const uint64_t b = vd + 512 * half;
-                            mma_ts4_warp(dov, dov, dov, dov, p, p + 8, p + 16, p + 24, b, b + 128, b + 256,
-                                         b + 384, kIdPV, i > 0 || half > 0, 1u);
+                        for (int part = 0; part < 2; ++part) {
+                            if (part == 1) {
+                                ok = warp_wait(&p_full[2 * t + 1], np & 1u, abort_flag, a.status, a.limit);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
+                            const uint32_t p = ds + 16 * part;
+                            const uint64_t b = vd + 256 * part;
+                            mma_ts4_warp(dov, dov, dov, dov, p, p + 8, p + 64, p + 72, b, b + 128, b + 512,
+                                         b + 640, kIdPV, i > 0 || part > 0, 1u);
                         }
+                        if (!ok) break;
+                        ++np;
                         mma_commit_warp(&pv_done[t]);
                         mma_commit_warp(&kv_empty[vslot]);
                     } else if (lane == 0) {
@@ -427,16 +475,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
     } else {
         reg_alloc<kRegsMany>();
-        // ---------------- softmax: thread = row ----------------
-        const int t = (warp - 4) >> 2;
+        // ---------------- softmax: row r of row tile t, keys [64 h, +64) of each key tile ----------------
+        const int t = (warp - 4) >> 3, h = ((warp - 4) >> 2) & 1;
         const int wq = warp & 3;
         const int r = wq * 32 + lane;
+        const int pair = 1 + 4 * t + wq;  // named barrier of the two warps that share rows
+        float *red = reinterpret_cast<float *>(sm + L::OFF_RED) + t * 256 + r;  // this row's maxima, then sums
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t scol = tmem + lane_base + 128 * t, ocol = tmem + lane_base + 256 + 128 * t;
+        const uint32_t scol = tmem + lane_base + 128 * t + 64 * h;
+        const uint32_t ocol = tmem + lane_base + 256 + 128 * t + (D / 2) * h;  // this half's share of O
         const int rt = r / G, rh = r % G;  // token of the tile, head of the group
         const float c = a.c;
+        const uint64_t c2 = f2_pack(c, c);
         uint32_t ns = 0;  // tiles this row tile has seen
-        bool ok = !*abort_flag;
+        bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
         for (uint32_t n = 0; ok; ++n) {
             const int us = n & 1;
             ok = __all_sync(0xffffffffu, wait_bar(&u_full[us], (n >> 1) & 1u, abort_flag, a.status, a.limit));
@@ -445,71 +497,74 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (!u.valid) break;
             const int et = u.e[t];
             const int tok = u.tok0 + t * tpt + rt;
-            const bool real = rt < tpt && tok < u.Lq;
-            int left, left0;  // last key of this row, and of the tile's first one, from the tile's first key
+            const bool real = rt < tpt && tok >= 0 && tok < u.Lq;
+            int left, left0;  // last key of this row, and of the tile's first one, from this half's first key
             {
-                const int Lk = u.Lk, j0 = u.j0, last = tok - rt + Lk - u.Lq;
-                left = (a.causal ? min(Lk - 1, last + rt) : Lk - 1) - j0 * kTileKeys;
-                // the first row keeps the fewest: key tiles that pass it are masked
-                left0 = (a.causal ? min(Lk - 1, last) : Lk - 1) - j0 * kTileKeys;
+                const int Lk = u.Lk, first = u.j0 * kTileKeys + 64 * h, last = tok - rt + Lk - u.Lq;
+                left = (a.causal ? min(Lk - 1, last + rt) : Lk - 1) - first;
+                // the first row keeps the fewest: key tiles that pass it are masked (both halves)
+                left0 = (a.causal ? min(Lk - 1, last) : Lk - 1) - u.j0 * kTileKeys;
             }
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f;  // m is the same in both halves
+            const bool exact = u.exact != 0;
+            bool over = false;
             for (int i = 0; i < et; ++i, ++ns, left -= kTileKeys, left0 -= kTileKeys) {
                 ok = wait_bar(&s_full[t], ns & 1u, abort_flag, a.status, a.limit) && ok;
                 tc_fence_after();
-                const uint64_t c2 = f2_pack(c, c);
-                const bool masked = kTileKeys - 1 > left0;  // uniform
-                bool done = false;
-                if (!masked && !__any_sync(0xffffffffu, real && m == -INFINITY)) {
-                    // against the reference that the row has; the loads run one part ahead
-                    const uint64_t nm2 = f2_pack(-m, -m);
-                    uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
-                    uint32_t pk[64];
-                    float s[2][32];
-                    tmem_ld32(scol, s[0]);
-                    tmem_wait_ld_of(s[0]);
+                const bool masked = kTileKeys - 1 > left0;  // uniform over the tile
+                auto hand_over = [&](int part) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * t + part]);
+                };
+                uint64_t ls2[2] = {0ull, 0ull};
+                if (i > 0 && !masked && !exact) {
+                    const uint64_t nm2 = f2_pack(-m, -m);  // (m is a number: the first tile was not masked)
 #pragma unroll
-                    for (int part = 0; part < 4; ++part) {
-                        if (part < 3) tmem_ld32(scol + 32 * (part + 1), s[(part + 1) & 1]);
-                        softmax_part<kPolyOf8>(s[part & 1], c2, nm2, ls2, pk + 16 * part);
-                        if (part < 3) tmem_wait_ld_of(s[(part + 1) & 1]);
+                    for (int part = 0; part < 2; ++part) {
+                        float s[32];
+                        uint32_t pk[16];
+                        tmem_ld32(scol + 32 * part, s);
+                        tmem_wait_ld_of(s);
+                        softmax_part<kPolyOf8>(s, c2, nm2, ls2, pk);
+                        tmem_st16(scol + 16 * part, pk);
+                        hand_over(part);
                     }
-                    const uint64_t ls = f2_add(f2_add(ls2[0], ls2[1]), f2_add(ls2[2], ls2[3]));
+                    const uint64_t ls = f2_add(ls2[0], ls2[1]);
                     const float sum = f2_lo(ls) + f2_hi(ls);
-                    // (not >: a NaN takes the other path too)
-                    done = !__any_sync(0xffffffffu, real && !(sum <= kMaxSum));
-                    if (done) {
-                        l += sum;
-                        tmem_st32(scol, reinterpret_cast<float *>(pk));
-                        tmem_st32(scol + 32, reinterpret_cast<float *>(pk + 32));
+                    over |= real && !(sum <= kMaxSum);  // (not >: a NaN counts)
+                    l += sum;
+                } else {
+                    // first, masked and exact tiles: the row's true maximum becomes its reference
+                    float s[32];
+                    auto scores = [&](int part) {
+                        tmem_ld32(scol + 32 * part, s);
+                        tmem_wait_ld_of(s);
+                        if (masked) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) s[k] = 32 * part + k <= left ? s[k] : -INFINITY;
+                        }
+                    };
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        scores(part);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) mx[(k >> 1) & 3] = fmax3(mx[(k >> 1) & 3], s[k], s[k + 1]);
                     }
-                }
-                if (!done) {
-                    // first, masked and exceptional tiles: the row's true maximum becomes its reference
-                    float s[128];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32(scol + 32 * q, s + 32 * q);
-                    tmem_wait_ld();
-                    if (masked) {
-#pragma unroll
-                        for (int k = 0; k < 128; ++k) s[k] = k <= left ? s[k] : -INFINITY;
-                    }
-                    float mx[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) mx[q] = s[q];
-#pragma unroll
-                    for (int k = 8; k < 128; k += 2) mx[(k >> 1) & 7] = fmax3(mx[(k >> 1) & 7], s[k], s[k + 1]);
-                    const float tmax = c * fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                                 fmaxf(mx[6], mx[7]));
-                    const float mnew = fmaxf(m, tmax);
-                    // warp-uniform decision: the TMEM accesses below are collective
+                    const float tmax = c * fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+                    red[128 * h] = tmax;
+                    bar_sync(pair, 64);
+                    const float mnew = fmax3(m, tmax, red[128 * (h ^ 1)]);
+                    // uniform over both warps' rows: the TMEM accesses below are collective
                     if (__any_sync(0xffffffffu, mnew > m)) {
                         const float alpha = m == -INFINITY ? 0.f : fast_exp2(m - mnew);
                         if (i > 0) {
                             ok = wait_bar(&pv_done[t], (ns - 1) & 1u, abort_flag, a.status, a.limit) && ok;
                             tc_fence_after();
 #pragma unroll
-                            for (int part = 0; part < D / 16; ++part) {
+                            for (int part = 0; part < D / 32; ++part) {
                                 float ov[16];
                                 tmem_ld16(ocol + 16 * part, ov);
                                 tmem_wait_ld();
@@ -523,36 +578,43 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     }
                     const float mref = m == -INFINITY ? 0.f : m;  // rows without a key so far
                     const uint64_t nm2 = f2_pack(-mref, -mref);
-                    uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-                    for (int part = 0; part < 4; ++part) {
+                    for (int part = 0; part < 2; ++part) {
                         uint32_t pk[16];
+                        scores(part);  // (their P goes over scores that were read before)
                         // masked scores are -inf: exactly 0 by the SFU, 2^-126 by the polynomial
-                        softmax_part<0>(s + 32 * part, c2, nm2, ls2, pk);
+                        softmax_part<0>(s, c2, nm2, ls2, pk);
                         tmem_st16(scol + 16 * part, pk);
+                        hand_over(part);
                     }
-                    const uint64_t ls = f2_add(f2_add(ls2[0], ls2[1]), f2_add(ls2[2], ls2[3]));
+                    const uint64_t ls = f2_add(ls2[0], ls2[1]);
                     l += f2_lo(ls) + f2_hi(ls);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[t]);
             }
-            // ---------------- epilogue ----------------
-            if (et > 0) ok = wait_bar(&pv_done[t], (ns - 1) & 1u, abort_flag, a.status, a.limit) && ok;
+            // ---------------- epilogue: half h writes features [D/2 h, +D/2) ----------------
+            bool again = false;
+            if (et > 0) {
+                ok = wait_bar(&pv_done[t], (ns - 1) & 1u, abort_flag, a.status, a.limit) && ok;
+                red[128 * h] = l;
+                again = bar_or(pair, 64, over);  // (and the sums are exchanged)
+                l += red[128 * (h ^ 1)];
+                bar_sync(pair, 64);  // read by both before the next unit's maxima
+                if (again && lane == 0) units[us].redo = 1;
+            }
             tc_fence_after();
             ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
             if (!ok) break;
             const int head = u.hk * G + rh;
             const int64_t grow = u.q0 + tok;
-            if (a.splits == 1) {
-                if (real && a.lse != nullptr)
+            if (again) {
+                // nothing of these rows is written this time
+            } else if (a.splits == 1) {
+                if (h == 0 && real && a.lse != nullptr)
                     a.lse[head * a.total_q + grow] = l > 0.f ? (m + log2f(l)) * kFwdLn2 : l == 0.f ? -INFINITY : l;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                __nv_bfloat16 *dst = a.o.row(grow, head);
+                __nv_bfloat16 *dst = a.o.row(grow, head) + (D / 2) * h;
 #pragma unroll
-                for (int part = 0; part < D / 32; ++part) {
+                for (int part = 0; part < D / 64; ++part) {
                     float ov[32];
                     if (et > 0) {
                         tmem_ld32(ocol + 32 * part, ov);
@@ -577,9 +639,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             } else {
                 // unnormalised part of this split: [split][token][head][D], then (m, l)
                 const int64_t slots = a.total_q * a.heads, slot = u.split * slots + grow * a.heads + head;
-                if (real) reinterpret_cast<float2 *>(a.part + a.splits * slots * D)[slot] = make_float2(m, l);
+                if (h == 0 && real)
+                    reinterpret_cast<float2 *>(a.part + a.splits * slots * D)[slot] = make_float2(m, l);
 #pragma unroll
-                for (int part = 0; part < D / 32; ++part) {
+                for (int part = 0; part < D / 64; ++part) {
                     float ov[32];
                     if (et > 0) {
                         tmem_ld32(ocol + 32 * part, ov);
@@ -591,7 +654,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     if (real) {
 #pragma unroll
                         for (int q = 0; q < 32; q += 4)
-                            *reinterpret_cast<float4 *>(a.part + slot * D + 32 * part + q) =
+                            *reinterpret_cast<float4 *>(a.part + slot * D + (D / 2) * h + 32 * part + q) =
                                 make_float4(ov[q], ov[q + 1], ov[q + 2], ov[q + 3]);
                     }
                 }

@@ -283,3 +283,23 @@ def test_backward_in_a_graph_and_zero_rows():
     assert bool((o1 == 0).all()) and bool((lse1 == -math.inf).all())
     dq, _, _ = nabla.attn_packed_bwd(q, k[:0], v[:0], o1, dout, lse1, cu_q, none)
     assert bool((dq == 0).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("step", [20.0, 80.0, 2000.0])
+def test_forward_scores_that_jump_far_above_the_first_tile(D, step):
+    """Some rows meet a key whose score lies `step` above all earlier ones, tiles
+    after the reference was set; others never do; lengths end inside tiles."""
+    lens = [900, 300, 140]
+    q, k, v, _, cq, ck, cu, _ = make(lens, lens, 4, 2, D, seed=13, std=0.5)
+    for a, b in zip(cq, cq[1:]):
+        n = b - a
+        for at in (n // 2, n - 3):
+            k[a + at, 0] = q[a + n - 1, 1] * (step / float(q[a + n - 1, 1].double().pow(2).sum() * D ** -0.5))
+    for causal in (False, True):
+        o, lse = run_fwd(q, k, v, cu, cu, causal)
+        r = seq_util.packed(q, k, v, cq, ck, causal)
+        # a score of s has a float32 error of up to D 2^-24 |s|, which enters P
+        e = D * 2.0 ** -24 * (step + 20)
+        seq_util.check(o, r["o"], r["o_tol"] * (1 + 4 * e / seq_util.H) + 4 * e * float(v.abs().max()), "o")
+        seq_util.check(lse, r["lse"], 2.0 ** -20 * (1 + r["lse"].abs()) + 2.0 ** -18 + e, "lse")
