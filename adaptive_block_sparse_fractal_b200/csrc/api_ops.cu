@@ -13,8 +13,7 @@
 // launchers (rope.cu, packed_fwd.cu, packed_bwd.cu, paged.cu)
 cudaError_t nabla_launch_rope(nabla::RopeArgs &a, int dtype, int layout, int wide,
                               cudaStream_t stream);
-cudaError_t nabla_launch_packed_fwd(const nabla::packed::Args &a, int D, int64_t units,
-                                    cudaStream_t stream);
+cudaError_t nabla_launch_packed_fwd(const nabla::packed::Args &a, int D, cudaStream_t stream);
 cudaError_t nabla_launch_packed_bwd(const nabla::packed::Args &a, int D, int64_t q_tiles,
                                     int64_t row_tiles, int64_t key_tiles, cudaStream_t stream);
 cudaError_t nabla_launch_append(const nabla::AppendArgs &a, cudaStream_t stream);
@@ -376,7 +375,8 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
     a.lse = lse;
     a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kStatusBytes);
     a.splits = splits;
-    return cuda_status(nabla_launch_packed_fwd(a, shape->D, units * splits, s));
+    a.units = units * splits;
+    return cuda_status(nabla_launch_packed_fwd(a, shape->D, s));
 }
 
 int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const nabla_view *k,

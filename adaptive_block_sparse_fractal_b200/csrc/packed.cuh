@@ -23,7 +23,7 @@ struct Args {
     int *status;       // workspace status word; behind it the forward's unit counter
     float *pad_l, *pad_d;  // backward: [heads, pad_rows], -lse log2(e) and -dout.o
     float *part;       // split forward: partial rows, then their (m, l)
-    int64_t total_q, total_k, pad_rows;
+    int64_t total_q, total_k, pad_rows, units;  // units: upper bound of the forward's
     int seqs, heads, heads_kv, group, causal;
     int tile_tokens, splits;  // forward: tokens a row tile (128 / group), splits of the key range
     float c, scale;    // scale * log2(e), scale

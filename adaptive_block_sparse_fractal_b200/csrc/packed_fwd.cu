@@ -242,9 +242,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 ++seq;
             };
             UnitScan scan;
-            int64_t x = lane == 0 ? take_unit(a) : 0;
-            bool more = true;
-            int ends = 0;
+            int64_t x = blockIdx.x;  // the first unit; the counter hands out those behind the grid's
             for (uint32_t n = 0; ok; ++n) {
                 // the slot's last unit is finished: it may have to be taken again
                 const int us = n & 1;
@@ -252,39 +250,43 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                                                    a.status, a.limit));
                 if (!ok) break;
                 Unit u = {};
-                const bool again = n >= 2 && units[us].redo != 0;
-                if (again) {
-                    u.valid = 1;
-                    u.exact = 1;
-                    u.hk = units[us].hk;
-                    u.split = units[us].split;
-                    u.q0 = units[us].q0;
-                    u.Lq = units[us].Lq;
-                    u.k0 = units[us].k0;
-                    u.Lk = units[us].Lk;
-                    u.tok0 = units[us].tok0;
-                    u.j0 = units[us].j0;
-                    u.e[0] = units[us].e[0];
-                    u.e[1] = units[us].e[1];
-                } else if (more) {
+                int again = n >= 2 && units[us].redo != 0 ? us : -1;
+                if (again < 0) {
                     x = __shfl_sync(0xffffffffu, x, 0);
                     const int64_t now = x;
-                    if (lane == 0) x = take_unit(a);  // the next one, under this one's loads
-                    const int64_t ux = now / a.splits;
-                    int tile = 0;
-                    u.split = static_cast<int>(now % a.splits);
-                    u.hk = static_cast<int>(ux % a.heads_kv);
-                    more = scan.find(a, ux / a.heads_kv, 2 * tpt, lane, &u.q0, &u.Lq, &u.k0, &u.Lk, &tile);
-                    u.valid = more ? 1 : 0;
-                    // the last tiles of a causal sequence keep the most keys: they go first
-                    u.tok0 = ((u.Lq + 2 * tpt - 1) / (2 * tpt) - 1 - tile) * 2 * tpt;
+                    if (now < a.units) {
+                        if (lane == 0) x = take_unit(a) + gridDim.x;  // the next one, under this one's loads
+                        const int64_t ux = now / a.splits;
+                        int tile = 0;
+                        u.split = static_cast<int>(now % a.splits);
+                        u.hk = static_cast<int>(ux % a.heads_kv);
+                        u.valid = scan.find(a, ux / a.heads_kv, 2 * tpt, lane, &u.q0, &u.Lq, &u.k0, &u.Lk, &tile);
+                        // the last tiles of a causal sequence keep the most keys: they go first
+                        if (u.valid) u.tok0 = ((u.Lq + 2 * tpt - 1) / (2 * tpt) - 1 - tile) * 2 * tpt;
+                    }
+                    if (!u.valid && n >= 1) {  // the end, unless the other slot's unit has to be taken again
+                        ok = __all_sync(0xffffffffu, lane != 0 || wait_bar(&u_empty[us ^ 1], ((n - 1) >> 1) & 1u,
+                                                                           abort_flag, a.status, a.limit));
+                        if (!ok) break;
+                        if (units[us ^ 1].redo != 0) again = us ^ 1;
+                    }
                 }
-                // behind the last unit: an empty one for each slot, in case the other
-                // slot's has to be taken again, then the end
-                const bool idle = !u.valid && ++ends <= 2;
-                if (!u.valid) u = {};  // no rows, no keys
-                if (idle) u.valid = 1;
-                if (u.valid && !again && !idle) {
+                if (again >= 0) {
+                    volatile Unit &w = units[again];
+                    u.valid = u.exact = 1;
+                    u.hk = w.hk;
+                    u.split = w.split;
+                    u.q0 = w.q0;
+                    u.Lq = w.Lq;
+                    u.k0 = w.k0;
+                    u.Lk = w.Lk;
+                    u.tok0 = w.tok0;
+                    u.j0 = w.j0;
+                    u.e[0] = w.e[0];
+                    u.e[1] = w.e[1];
+                    __syncwarp();
+                    if (lane == 0) w.redo = 0;
+                } else if (u.valid) {
                     const int off = u.Lk - u.Lq;
                     int kt[2];
 #pragma unroll
@@ -300,7 +302,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     u.e[0] = max(0, min(j1, kt[0]) - u.j0);
                     u.e[1] = max(0, min(j1, kt[1]) - u.j0);
                 }
-                if (again) ends = 0;
                 const int emax = max(u.e[0], u.e[1]);
                 __syncwarp();
                 if (lane == 0) {
@@ -383,14 +384,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (lane == 0) mbar_arrive(&turn[t ^ 1]);
                 __syncwarp();
             };
+            // at D = 128 the turn passes in front of the last four MMAs, whose run hides
+            // the change (1,257 against 1,240 TFLOP/s); at D = 64 there are only four,
+            // and passing in front of them lost 7%
             auto S = [&]() {
                 const uint64_t kd = desc_sw128(sb + L::OFF_RING + slot * kTile, 16, 1024);
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) {
+                    if (h == 1) pass_turn();
                     const uint32_t o = h * 1024;  // halves 16 KB, 16 features 32 bytes
                     mma_ss4_warp(ds, ds, ds, ds, qd + o, qd + o + 2, qd + o + 4, qd + o + 6, kd + o, kd + o + 2,
                                  kd + o + 4, kd + o + 6, kIdS, h > 0, 1u);
                 }
+                if (kHalves == 1) pass_turn();
             };
             for (uint32_t n = 0; ok; ++n) {
                 const int us = n & 1;
@@ -416,10 +422,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     mma_commit_warp(&s_full[t]);
                     mma_commit_warp(&kv_empty[slot]);
                     if (e == 1) mma_commit_warp(&q_empty[t]);
-                } else if (lane == 0) {
-                    mbar_arrive(&kv_empty[slot]);
+                } else {
+                    if (lane == 0) mbar_arrive(&kv_empty[slot]);
+                    pass_turn();
                 }
-                pass_turn();
                 next();
                 for (int i = 0; ok && i < emax; ++i) {
                     const bool more = i + 1 < emax;
@@ -454,6 +460,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     } else if (lane == 0) {
                         mbar_arrive(&kv_empty[vslot]);
                     }
+                    if (i + 1 >= e) pass_turn();
                     if (more) {
                         if (i + 1 < e) {
                             S();
@@ -465,7 +472,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         }
                         next();
                     }
-                    pass_turn();
                 }
             }
             // completes once every MMA that this warp issued has finished
@@ -745,7 +751,7 @@ bool nabla_make_tmap_view(CUtensorMap *m, const nabla::packed::View &v, int64_t 
 }
 
 template <int D>
-static cudaError_t launch_packed_fwd(const nabla::packed::Args &a, int64_t units, cudaStream_t stream) {
+static cudaError_t launch_packed_fwd(const nabla::packed::Args &a, cudaStream_t stream) {
     using namespace nabla::packed;
     CUtensorMap mq, mk, mv;
     // without any key nothing is loaded; the maps only have to be valid
@@ -758,7 +764,7 @@ static cudaError_t launch_packed_fwd(const nabla::packed::Args &a, int64_t units
     cudaError_t err = cudaFuncSetAttribute(fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(kSmem));
     if (err != cudaSuccess) return err;
-    const unsigned grid = static_cast<unsigned>(units < kSms ? units : kSms);
+    const unsigned grid = static_cast<unsigned>(a.units < kSms ? a.units : kSms);
     fwd_kernel<D><<<grid, kFwdThreads, kSmem, stream>>>(mq, mk, mv, a);
     err = cudaGetLastError();
     if (err != cudaSuccess || a.splits == 1) return err;
@@ -767,8 +773,6 @@ static cudaError_t launch_packed_fwd(const nabla::packed::Args &a, int64_t units
     return cudaGetLastError();
 }
 
-// units: row tile pairs (an upper bound over the sequences) x heads_kv x splits
-cudaError_t nabla_launch_packed_fwd(const nabla::packed::Args &a, int D, int64_t units,
-                                    cudaStream_t stream) {
-    return D == 128 ? launch_packed_fwd<128>(a, units, stream) : launch_packed_fwd<64>(a, units, stream);
+cudaError_t nabla_launch_packed_fwd(const nabla::packed::Args &a, int D, cudaStream_t stream) {
+    return D == 128 ? launch_packed_fwd<128>(a, stream) : launch_packed_fwd<64>(a, stream);
 }

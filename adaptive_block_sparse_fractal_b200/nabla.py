@@ -4,7 +4,6 @@ Argument marshalling only: torch tensors provide device memory and the
 current CUDA stream; every step runs in the library's kernels.  There is no
 fallback: if the library is missing or a call fails, this module raises.
 """
-import contextlib
 import ctypes
 import os
 
@@ -147,7 +146,8 @@ def _check(status, what):
 
 
 def _stream(t):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    """The current stream of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t):
@@ -317,50 +317,61 @@ def attn_bwd(shape, params, q, k, v, o, dout, lse, mask, dq=None, dk=None, dv=No
 # ---------------------------------------------------------------------------
 # rotary positions, packed-sequence attention, the paged cache
 # ---------------------------------------------------------------------------
-_no_change = contextlib.nullcontext()
+def _call(fn, what, dev, *args):
+    """fn(*args, current stream of device dev), launched on that device."""
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status != OK:
+        raise NablaError(status, what)
 
 
-def _on(t):
-    """The tensor's device as the current one (the library launches there)."""
-    if torch.cuda.current_device() == t.device.index:
-        return _no_change
-    return torch.cuda.device(t.device)
+def _device(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return dev
 
 
-def _rows(t, dims, dtype, name, like=None):
-    """A CUDA tensor of `dims` dimensions whose rows are contiguous."""
-    if not (t.is_cuda and t.dtype == dtype and t.dim() == dims):
-        raise ValueError("%s must be a CUDA %s tensor of %d dimensions" % (name, dtype, dims))
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError("%s: the last dimension must be contiguous" % name)
-    if like is not None and t.device != like.device:
-        raise ValueError("%s must be on %s" % (name, like.device))
-    return t
-
-
-def _ints(t, shape, name, like):
-    if not (t.is_cuda and t.dtype == torch.int32 and t.is_contiguous() and t.device == like.device):
-        raise ValueError("%s must be a contiguous int32 tensor on %s" % (name, like.device))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+def _view(t, name, dev, dims, dtype, shape=None):
+    """(data, batch, head, token) of a tensor of rows on device dev.  Its last
+    dimension is contiguous; in front of it stand the tokens and heads ([tokens,
+    heads, D], dims = 3) or pages, rows and heads (dims = 4)."""
+    s = t.stride()
+    if t.dtype != dtype or t.get_device() != dev or len(s) != dims or s[-1] != 1:
+        raise ValueError("%s must be a %s tensor of %d dimensions on cuda:%d with a contiguous last "
+                         "dimension" % (name, dtype, dims, dev))
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    return t
+    return (t.data_ptr(), 0, s[1], s[0]) if dims == 3 else (t.data_ptr(), s[0], s[2], s[1])
 
 
-def _same(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+def _views(*views):
+    """References to consecutive nabla_view structures."""
+    a = (ctypes.c_int64 * (4 * len(views)))(*[x for v in views for x in v])
+    return [ctypes.byref(a, 32 * i) for i in range(len(views))]
+
+
+def _int32(t, name, dev, shape=None):
+    if t.dtype != torch.int32 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor on cuda:%d" % (name, dev))
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
 
 
-def _work(ws, like):
-    if not (ws.is_cuda and ws.device == like.device and ws.dtype == torch.uint8 and
-            ws.is_contiguous()):
-        raise ValueError("ws must be a contiguous uint8 tensor on %s" % like.device)
-    return ws
+def _lse(t, dev, shape):
+    if t.dtype != torch.float32 or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
+        raise ValueError("lse must be a contiguous float32 tensor %s on cuda:%d" % (tuple(shape), dev))
+    return t.data_ptr()
 
 
-def _tokens(t):
-    """Reference to the view of a [tokens, heads, D] tensor."""
-    return ctypes.byref(View(t.data_ptr(), 0, t.stride(1), t.stride(0)))
+def _work(ws, dev):
+    if ws.dtype != torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 tensor on cuda:%d" % dev)
+    return ws.data_ptr(), ws.numel()
 
 
 def rope_params_of(pairs, theta=10000.0, scale=1.0, offset=0.0, layout=ROPE_ADJACENT,
@@ -390,60 +401,61 @@ def rope(params, q, k=None, grid=None, pos=None, flat_in=False, flat_out=False, 
     by `pos` (int32 [N, axes] or [B, N, axes], in grid order).  flat_in /
     flat_out: that side is in flattened token order (needs `grid`).  Outputs may
     be the inputs (same order on both sides).  Returns q_out, or (q_out, k_out)."""
-    dims = q.dim()
-    if dims not in (3, 4) or q.dtype not in DTYPES:
+    dtype, shape = q.dtype, q.shape
+    dims = len(shape)
+    if dims not in (3, 4) or dtype not in DTYPES:
         raise ValueError("q must be [B, heads, N, D] or [heads, N, D] in bf16, fp16 or fp32")
-    N, D = q.shape[-2:]
-    B = q.shape[0] if dims == 4 else 1
+    dev = _device(q, "q")
+    N, D = shape[-2:]
+    B = shape[0] if dims == 4 else 1
     if grid is None:
         if pos is None or flat_in or flat_out:
             raise ValueError("grid is needed without pos and for a flattened order")
         grid = (N, 1, 1)
-    T, H, W = (int(n) for n in grid)
+    T, H, W = grid
     if T * H * W != N:
         raise ValueError("grid %s does not hold %d tokens" % (tuple(grid), N))
-    ins = [q] if k is None else [q, k]
-    outs = [q_out] if k is None else [q_out, k_out]
-    heads = (ctypes.c_int * 2)()
-    vi, vo = (View * 2)(), (View * 2)()
-    for i, x in enumerate(ins):
-        _rows(x, dims, q.dtype, "qk"[i], q)
-        if x.shape[-2:] != q.shape[-2:] or (dims == 4 and x.shape[0] != B):
+    values, heads = [[], []], (ctypes.c_int * 2)()
+    results = []
+    for i, (x, y) in enumerate(((q, q_out), (k, k_out))):
+        if x is None:
+            break
+        if i and (x.shape[-2:] != shape[-2:] or x.dim() != dims or (dims == 4 and x.shape[0] != B)):
             raise ValueError("q and k must have the same batch, tokens and D")
-        if outs[i] is None:
-            outs[i] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        y = _rows(outs[i], dims, q.dtype, "qk"[i] + "_out", q)
-        _same(y, x.shape, "qk"[i] + "_out")
+        if y is None:
+            y = torch.empty_like(x)
+        elif y.shape != x.shape:
+            raise ValueError("an output must have its input's shape")
+        results.append(y)
         heads[i] = x.shape[-3]
-        for t, v in ((x, vi[i]), (y, vo[i])):
-            v.data, v.batch = t.data_ptr(), t.stride(0) if dims == 4 else 0
-            v.head, v.token = t.stride(-3), t.stride(-2)
-    pos_batch, axes = 0, 0
+        for side, t in ((0, x), (1, y)):
+            s = t.stride()
+            if t.dtype != dtype or t.get_device() != dev or (s[-1] != 1 and D > 1):
+                raise ValueError("q, k and the outputs must be %s tensors on cuda:%d with contiguous rows"
+                                 % (dtype, dev))
+            values[side] += (t.data_ptr(), s[0] if dims == 4 else 0, s[-3], s[-2])
+    pos_ptr, pos_batch, axes = None, 0, 0
     if pos is not None:
         axes = pos.shape[-1]
-        _ints(pos, (N, axes) if pos.dim() == 2 else (B, N, axes), "pos", q)
+        pos_ptr = _int32(pos, "pos", dev, (N, axes) if pos.dim() == 2 else (B, N, axes))
         pos_batch = N * axes if pos.dim() == 3 else 0
     p = RopeParams.from_buffer_copy(params)
-    p.dtype, p.D = DTYPES[q.dtype], D
+    p.dtype, p.D = DTYPES[dtype], D
     p.flags |= (ROPE_FLAT_IN if flat_in else 0) | (ROPE_FLAT_OUT if flat_out else 0)
-    with _on(q):
-        _check(lib().nabla_rope(ctypes.byref(p), B, T, H, W, int(P), len(ins), heads, vi, vo,
-                                _ptr(pos), pos_batch, axes, _stream(q)), "nabla_rope")
-    return outs[0] if k is None else (outs[0], outs[1])
+    n = len(results)
+    _call(lib().nabla_rope, "nabla_rope", dev, ctypes.byref(p), B, T, H, W, P, n, heads,
+          (ctypes.c_int64 * (4 * n))(*values[0]), (ctypes.c_int64 * (4 * n))(*values[1]), pos_ptr,
+          pos_batch, axes)
+    return results[0] if k is None else tuple(results)
 
 
-def _packed_of(q, k, v, cu_q, cu_k, causal, scale):
-    _rows(q, 3, torch.bfloat16, "q")
-    _rows(k, 3, torch.bfloat16, "k", q)
-    _rows(v, 3, torch.bfloat16, "v", q)
-    _same(v, k.shape, "v")
-    if k.shape[2] != q.shape[2]:
-        raise ValueError("q and k must have the same D")
-    _ints(cu_q, (cu_q.numel(),), "cu_q", q)
-    _ints(cu_k, cu_q.shape, "cu_k", q)
-    D = q.shape[2]
-    return Packed(cu_q.numel() - 1, q.shape[1], k.shape[1], D, q.shape[0], k.shape[0],
-                  int(bool(causal)), float(D ** -0.5 if scale is None else scale))
+def _packed_of(q, k, cu_q, causal, scale):
+    shape = q.shape
+    D = shape[-1]
+    if k.shape[-1] != D or len(shape) != 3:
+        raise ValueError("q must be [total_q, heads, D] and k [total_k, heads_kv, D]")
+    return Packed(cu_q.shape[0] - 1, shape[1], k.shape[1], D, shape[0], k.shape[0],
+                  1 if causal else 0, D ** -0.5 if scale is None else scale)
 
 
 def packed_workspace(q, k, seqs, back=False):
@@ -462,57 +474,54 @@ def attn_packed_fwd(q, k, v, cu_q, cu_k, causal=False, scale=None, o=None, lse=N
     """Attention of packed sequences: q [total_q, heads, D], k, v [total_k,
     heads_kv, D] (bf16, any strides of 16 bytes with contiguous rows), borders
     cu_q, cu_k int32 [seqs + 1].  causal aligns the last rows of q and k.
-    Returns o [total_q, heads, D] and lse float32 [heads, total_q]; rows of no
+    Returns o (laid out like q) and lse float32 [heads, total_q]; rows of no
     sequence are left as they were."""
-    s = _packed_of(q, k, v, cu_q, cu_k, causal, scale)
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
-    _same(_rows(o, 3, torch.bfloat16, "o", q), q.shape, "o")
+    dev = _device(q, "q")
+    bf = torch.bfloat16
+    shape = _packed_of(q, k, cu_q, causal, scale)
+    views = [_view(q, "q", dev, 3, bf), _view(k, "k", dev, 3, bf), _view(v, "v", dev, 3, bf, k.shape)]
+    if o is None:
+        o = torch.empty_like(q)
+    views.append(_view(o, "o", dev, 3, bf, q.shape))
     if lse is None and want_lse:
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _need(lse, torch.float32, "lse")
-        _same(lse, (q.shape[1], q.shape[0]), "lse")
-    ws = packed_workspace(q, k, s.seqs) if ws is None else _work(ws, q)
-    with _on(q):
-        _check(lib().nabla_attn_packed_fwd(ctypes.byref(s), _tokens(q), _tokens(k), _tokens(v),
-                                           _ptr(cu_q), _ptr(cu_k), _tokens(o), _ptr(lse), _ptr(ws),
-                                           ws.numel(), _stream(q)), "nabla_attn_packed_fwd")
+        lse = q.new_empty((q.shape[1], q.shape[0]), dtype=torch.float32)
+    lse_ptr = None if lse is None else _lse(lse, dev, (q.shape[1], q.shape[0]))
+    ws, ws_bytes = _work(packed_workspace(q, k, shape.seqs) if ws is None else ws, dev)
+    vq, vk, vv, vo = _views(*views)
+    _call(lib().nabla_attn_packed_fwd, "nabla_attn_packed_fwd", dev, ctypes.byref(shape), vq, vk, vv,
+          _int32(cu_q, "cu_q", dev), _int32(cu_k, "cu_k", dev, cu_q.shape), vo, lse_ptr, ws, ws_bytes)
     return o, lse
 
 
 def attn_packed_bwd(q, k, v, o, dout, lse, cu_q, cu_k, causal=False, scale=None, dq=None, dk=None,
                     dv=None, ws=None):
     """Gradients dq, dk, dv of attn_packed_fwd from its o and lse."""
-    s = _packed_of(q, k, v, cu_q, cu_k, causal, scale)
-    for t, n in ((o, "o"), (dout, "dout")):
-        _same(_rows(t, 3, torch.bfloat16, n, q), q.shape, n)
-    _need(lse, torch.float32, "lse")
-    _same(lse, (q.shape[1], q.shape[0]), "lse")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
-    for t, like, n in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
-        _same(_rows(t, 3, torch.bfloat16, n, q), like.shape, n)
-    ws = packed_workspace(q, k, s.seqs, back=True) if ws is None else _work(ws, q)
-    with _on(q):
-        _check(lib().nabla_attn_packed_bwd(ctypes.byref(s), _tokens(q), _tokens(k), _tokens(v),
-                                           _tokens(o), _tokens(dout), _ptr(lse), _ptr(cu_q),
-                                           _ptr(cu_k), _tokens(dq), _tokens(dk), _tokens(dv),
-                                           _ptr(ws), ws.numel(), _stream(q)),
-               "nabla_attn_packed_bwd")
+    dev = _device(q, "q")
+    bf = torch.bfloat16
+    shape = _packed_of(q, k, cu_q, causal, scale)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    qs, ks = q.shape, k.shape
+    vq, vk, vv, vo, vg, wq, wk, wv = _views(
+        _view(q, "q", dev, 3, bf), _view(k, "k", dev, 3, bf), _view(v, "v", dev, 3, bf, ks),
+        _view(o, "o", dev, 3, bf, qs), _view(dout, "dout", dev, 3, bf, qs),
+        _view(dq, "dq", dev, 3, bf, qs), _view(dk, "dk", dev, 3, bf, ks), _view(dv, "dv", dev, 3, bf, ks))
+    lse_ptr = _lse(lse, dev, (qs[1], qs[0]))
+    ws, ws_bytes = _work(packed_workspace(q, k, shape.seqs, back=True) if ws is None else ws, dev)
+    _call(lib().nabla_attn_packed_bwd, "nabla_attn_packed_bwd", dev, ctypes.byref(shape), vq, vk, vv, vo,
+          vg, lse_ptr, _int32(cu_q, "cu_q", dev), _int32(cu_k, "cu_k", dev, cu_q.shape), wq, wk, wv, ws,
+          ws_bytes)
     return dq, dk, dv
 
 
-def _cache_of(k_cache, v_cache, table, seqs):
-    _rows(k_cache, 4, torch.bfloat16, "k_cache")
-    _rows(v_cache, 4, torch.bfloat16, "v_cache", k_cache)
-    _same(v_cache, k_cache.shape, "v_cache")
-    pages, page, heads_kv, D = k_cache.shape
-    if table is not None:
-        _ints(table, (seqs, table.shape[-1]), "table", k_cache)
-    kv = [View(t.data_ptr(), t.stride(0), t.stride(2), t.stride(1)) for t in (k_cache, v_cache)]
-    return Cache(kv[0], kv[1], _ptr(table), pages, page, heads_kv, D, seqs,
-                 1 if table is None else table.shape[1])
+def _cache_of(k_cache, v_cache, table, seqs, dev):
+    shape = k_cache.shape
+    k = _view(k_cache, "k_cache", dev, 4, torch.bfloat16)
+    v = _view(v_cache, "v_cache", dev, 4, torch.bfloat16, shape)
+    width = 1 if table is None else table.shape[-1]
+    ptr = None if table is None else _int32(table, "table", dev, (seqs, width))
+    return Cache(View(*k), View(*v), ptr, shape[0], shape[1], shape[2], shape[3], seqs, width)
 
 
 def cache_workspace(device):
@@ -526,24 +535,22 @@ def cache_append(k, v, k_cache, v_cache, table, starts, cu=None, ws=None):
     D] behind the starts[s] rows that sequence s has.  table int32 [seqs,
     width].  Rows without a page are skipped; with `ws` (cache_workspace) they
     are reported by status(ws)."""
+    dev = _device(k, "k")
     seqs = starts.numel()
-    _ints(starts, (seqs,), "starts", k)
-    if cu is not None:
-        _ints(cu, (seqs + 1,), "cu", k)
-    c = _cache_of(k_cache, v_cache, table, seqs)
-    for t, n in ((k, "k"), (v, "v")):
-        _same(_rows(t, 3, torch.bfloat16, n, k_cache), (k.shape[0], c.heads_kv, c.D), n)
-    with _on(k):
-        _check(lib().nabla_cache_append(ctypes.byref(c), _tokens(k), _tokens(v), k.shape[0],
-                                        _ptr(starts), _ptr(cu),
-                                        None if ws is None else _ptr(_work(ws, k)),
-                                        0 if ws is None else ws.numel(), _stream(k)),
-               "nabla_cache_append")
+    starts_ptr = _int32(starts, "starts", dev, (seqs,))
+    cu_ptr = None if cu is None else _int32(cu, "cu", dev, (seqs + 1,))
+    c = _cache_of(k_cache, v_cache, table, seqs, dev)
+    if tuple(k.shape[1:]) != (c.heads_kv, c.D):
+        raise ValueError("k must be [total, %d, %d]" % (c.heads_kv, c.D))
+    vk, vv = _views(_view(k, "k", dev, 3, torch.bfloat16), _view(v, "v", dev, 3, torch.bfloat16, k.shape))
+    ws, ws_bytes = (None, 0) if ws is None else _work(ws, dev)
+    _call(lib().nabla_cache_append, "nabla_cache_append", dev, ctypes.byref(c), vk, vv, k.shape[0],
+          starts_ptr, cu_ptr, ws, ws_bytes)
 
 
 def paged_workspace(q, k_cache):
     """Workspace of attn_paged; it serves one call at a time."""
-    c = _cache_of(k_cache, k_cache, None, 0)
+    c = _cache_of(k_cache, k_cache, None, 0, _device(k_cache, "k_cache"))
     n = int(lib().nabla_paged_workspace_size(ctypes.byref(c), q.shape[1]))
     if n == 0:
         raise NablaError(ERR_SHAPE, "nabla_paged_workspace_size")
@@ -554,25 +561,24 @@ def attn_paged(q, k_cache, v_cache, table, lens, scale=None, o=None, lse=None, w
                want_lse=True):
     """Attention of one new token per sequence, q [seqs, heads, D], over the
     first lens[s] rows of its pages.  Returns o and lse float32 [seqs, heads]."""
-    _rows(q, 3, torch.bfloat16, "q", k_cache)
-    seqs, heads, D = q.shape
-    c = _cache_of(k_cache, v_cache, table, seqs)
+    dev = _device(q, "q")
+    bf = torch.bfloat16
+    shape = q.shape
+    view = _view(q, "q", dev, 3, bf)
+    seqs, heads, D = shape
+    c = _cache_of(k_cache, v_cache, table, seqs, dev)
     if c.D != D:
         raise ValueError("q and the cache must have the same D")
-    _ints(lens, (seqs,), "lens", q)
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
-    _same(_rows(o, 3, torch.bfloat16, "o", q), q.shape, "o")
+    if o is None:
+        o = torch.empty_like(q)
     if lse is None and want_lse:
-        lse = torch.empty((seqs, heads), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _need(lse, torch.float32, "lse")
-        _same(lse, (seqs, heads), "lse")
-    ws = paged_workspace(q, k_cache) if ws is None else _work(ws, q)
-    with _on(q):
-        _check(lib().nabla_attn_paged(ctypes.byref(c), heads,
-                                      float(D ** -0.5 if scale is None else scale), _tokens(q),
-                                      _ptr(lens), _tokens(o), _ptr(lse), _ptr(ws), ws.numel(),
-                                      _stream(q)), "nabla_attn_paged")
+        lse = q.new_empty((seqs, heads), dtype=torch.float32)
+    lse_ptr = None if lse is None else _lse(lse, dev, (seqs, heads))
+    vq, vo = _views(view, _view(o, "o", dev, 3, bf, shape))
+    ws, ws_bytes = _work(paged_workspace(q, k_cache) if ws is None else ws, dev)
+    _call(lib().nabla_attn_paged, "nabla_attn_paged", dev, ctypes.byref(c), heads,
+          D ** -0.5 if scale is None else scale, vq, _int32(lens, "lens", dev, (seqs,)), vo, lse_ptr, ws,
+          ws_bytes)
     return o, lse
 
 
