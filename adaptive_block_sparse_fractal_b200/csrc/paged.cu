@@ -40,76 +40,78 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kAppendTokens = 8;  // most tokens a CTA takes
 
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendArgs a, int per_cta) {
-    __shared__ int64_t place_k[kAppendTokens], place_v[kAppendTokens];
+    constexpr int U = 4;  // pieces a thread has in flight
+    __shared__ int64_t place[2][kAppendTokens];
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * per_cta;
-    if (threadIdx.x < per_cta) {
+    const int tokens = static_cast<int>(a.total - t0 < per_cta ? a.total - t0 : per_cta);
+    const int chunks = a.c.D / 8;                // 16-byte pieces a row
+    const int row = a.c.heads_kv * chunks;       // pieces of all heads
+    const int n = tokens * row * 2;              // K and V
+    uint4 w[U];
+    int64_t at[U];  // in the page row: element offset; the token in `who`
+    int who[U];
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int x = base + u * 256;
+            who[u] = -1;
+            if (x < n) {
+                const int which = x % row, tv = x / row, j = tv >> 1, h = which / chunks, c = which % chunks;
+                who[u] = tv;
+                at[u] = ((tv & 1) ? h * a.c.v_head : h * a.c.k_head) + 8 * c;
+                const __nv_bfloat16 *src = (tv & 1) ? a.v + (t0 + j) * a.v_token + h * a.v_head
+                                                    : a.k + (t0 + j) * a.k_token + h * a.k_head;
+                w[u] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+            }
+        }
+    };
+    fetch(threadIdx.x);  // the first pieces travel while the places are looked up
+    if (threadIdx.x < tokens) {
         const int64_t tok = t0 + threadIdx.x;
         int64_t pk = -1, pv = -1;
         int s = -1;
         int64_t i = 0;
-        if (tok < a.total) {
-            if (a.cu == nullptr) {
-                s = static_cast<int>(tok);
-            } else if (tok >= a.cu[0] && tok < a.cu[a.c.seqs]) {
-                int lo = 0, hi = a.c.seqs;  // last s with cu[s] <= tok
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (a.cu[mid] <= tok)
-                        lo = mid;
-                    else
-                        hi = mid;
-                }
-                s = lo;
-                i = tok - a.cu[s];
+        if (a.cu == nullptr) {
+            s = static_cast<int>(tok);
+        } else if (tok >= a.cu[0] && tok < a.cu[a.c.seqs]) {
+            int lo = 0, hi = a.c.seqs;  // last s with cu[s] <= tok
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (a.cu[mid] <= tok)
+                    lo = mid;
+                else
+                    hi = mid;
             }
-            if (s >= 0) {
-                const int64_t p = a.starts[s] + i;
-                const int64_t col = p / a.c.page_size;
-                int page = -1;
-                if (p >= 0 && i >= 0 && col < a.c.width)
-                    page = a.c.table[static_cast<int64_t>(s) * a.c.width + col];
-                if (page >= 0 && page < a.c.pages) {
-                    const int64_t r = p - col * a.c.page_size;
-                    pk = page * a.c.k_page + r * a.c.k_token;
-                    pv = page * a.c.v_page + r * a.c.v_token;
-                } else if (a.status != nullptr) {
-                    atomicExch(a.status, kDevParam);
-                }
+            s = lo;
+            i = tok - a.cu[s];
+        }
+        if (s >= 0) {
+            const int64_t p = a.starts[s] + i;
+            const int64_t col = p / a.c.page_size;
+            int page = -1;
+            if (p >= 0 && i >= 0 && col < a.c.width)
+                page = a.c.table[static_cast<int64_t>(s) * a.c.width + col];
+            if (page >= 0 && page < a.c.pages) {
+                const int64_t r = p - col * a.c.page_size;
+                pk = page * a.c.k_page + r * a.c.k_token;
+                pv = page * a.c.v_page + r * a.c.v_token;
+            } else if (a.status != nullptr) {
+                atomicExch(a.status, kDevParam);
             }
         }
-        place_k[threadIdx.x] = pk;
-        place_v[threadIdx.x] = pv;
+        place[0][threadIdx.x] = pk;
+        place[1][threadIdx.x] = pv;
     }
     __syncthreads();
-    const int chunks = a.c.D / 8;                // 16-byte pieces a row
-    const int row = a.c.heads_kv * chunks;       // pieces of all heads
-    const int64_t n = static_cast<int64_t>(per_cta) * row * 2;  // K and V
-    const int stride = blockDim.x;
-    for (int64_t base = threadIdx.x; base < n; base += 4 * stride) {
-        uint4 w[4];
-        __nv_bfloat16 *dst[4];
+    for (int base = threadIdx.x; base < n; base += U * 256) {
+        if (base != threadIdx.x) fetch(base);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int64_t x = base + u * stride;
-            dst[u] = nullptr;
-            if (x < n) {
-                const int which = static_cast<int>(x % row);
-                const int tv = static_cast<int>(x / row);
-                const int j = tv >> 1;
-                const bool is_v = tv & 1;
-                const int h = which / chunks, c = which % chunks;
-                const int64_t place = is_v ? place_v[j] : place_k[j];
-                if (place >= 0) {
-                    const __nv_bfloat16 *src = is_v ? a.v + (t0 + j) * a.v_token + h * a.v_head
-                                                    : a.k + (t0 + j) * a.k_token + h * a.k_head;
-                    w[u] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-                    dst[u] = (is_v ? a.c.v + place + h * a.c.v_head : a.c.k + place + h * a.c.k_head) + 8 * c;
-                }
-            }
+        for (int u = 0; u < U; ++u) {
+            if (who[u] < 0) continue;
+            const int64_t p = place[who[u] & 1][who[u] >> 1];
+            if (p >= 0)
+                *reinterpret_cast<uint4 *>(((who[u] & 1) ? a.c.v : a.c.k) + p + at[u]) = w[u];
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (dst[u] != nullptr) *reinterpret_cast<uint4 *>(dst[u]) = w[u];
     }
 }
 
@@ -172,8 +174,19 @@ constexpr uint32_t smem_bytes() {
     return kWarps * kStages * stage_bytes<D>();
 }
 
-// The share of CTA c of W units: [W c / n, W (c + 1) / n)
+// CTAs that share W units: no more than there are units
+__device__ __forceinline__ int sharers(int64_t W, int ctas) { return W < ctas ? static_cast<int>(W) : ctas; }
+// The share of CTA c of n: [W c / n, W (c + 1) / n), never empty
 __device__ __forceinline__ int64_t share(int64_t W, int c, int n) { return W * c / n; }
+
+// Programmatic dependent launch: the join starts beside the attention, up to
+// its wait, which returns when the attention has finished.
+__device__ __forceinline__ void allow_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_prerequisites() {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const __grid_constant__ PagedArgs a) {
@@ -187,24 +200,39 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const __grid_constan
     if (threadIdx.x == 0) any_bad = 0;
     bool bad = false;
 
+    allow_dependents();
     // this CTA's run of units
-    int64_t zero, tiles;
-    tile_sums<kThreads>(a, 0, sums, &zero, &tiles);
+    const int first_len = threadIdx.x < a.c.seqs ? clean_len(a, threadIdx.x, &bad) : 0;
+    int64_t tiles = 0;
+    {
+        for (int i = threadIdx.x; i < a.c.seqs; i += kThreads)
+            tiles += tiles_of(i == threadIdx.x ? first_len : clean_len(a, i, &bad));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        if (lane == 0) sums[kWarps + warp] = tiles;
+        __syncthreads();
+        tiles = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) tiles += sums[kWarps + w];
+    }
     const int64_t W = tiles * per_seq;
-    const int64_t u0 = share(W, blockIdx.x, gridDim.x), u1 = share(W, blockIdx.x + 1, gridDim.x);
+    const int n_share = sharers(W, gridDim.x);
+    const bool mine = static_cast<int>(blockIdx.x) < n_share;
+    const int64_t u0 = mine ? share(W, blockIdx.x, n_share) : 0, u1 = mine ? share(W, blockIdx.x + 1, n_share) : 0;
     if (u0 < u1) {
         // the sequence of unit u0: scans of kThreads sequences at a time
         int64_t carry = 0;
         for (int base = 0; base < a.c.seqs; base += kThreads) {
             const int s = base + threadIdx.x;
-            const int64_t n = s < a.c.seqs ? static_cast<int64_t>(tiles_of(clean_len(a, s, &bad))) * per_seq : 0;
+            const int len = base == 0 ? first_len : s < a.c.seqs ? clean_len(a, s, &bad) : 0;
+            const int64_t n = static_cast<int64_t>(tiles_of(len)) * per_seq;
             int64_t incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += t;
             }
-            __syncthreads();
+            if (base > 0) __syncthreads();
             if (lane == 31) sums[warp] = incl;
             __syncthreads();
             int64_t front = carry;
@@ -457,13 +485,25 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ PagedArgs a) {
     constexpr int kPer = D / 32;
     __shared__ int64_t sums[2 * kWarps];
-    __shared__ float so[kWarps][D], sml[kWarps][2];
+    __shared__ float so[kWarps][D], sw[kPagedCtas], part[2][kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
     int64_t front, tiles;
     tile_sums<kThreads>(a, s, sums, &front, &tiles);
     bool bad = false;
     const int nt = tiles_of(clean_len(a, s, &bad));
+    const int per_seq = a.c.heads_kv * a.chunks;
+    const int hk = head / a.group, g = head % a.group;
+    const int pair = hk * a.chunks + g / kPagedHeads, r = g % kPagedHeads;
+    const int64_t W = tiles * per_seq, first = front * per_seq + static_cast<int64_t>(pair) * nt;
+    const int n = sharers(W, a.ctas);
+    // the CTA of unit u is the last one whose share begins at or before it
+    int c0 = 0, c1 = 0;
+    if (nt > 0) {
+        c0 = static_cast<int>(((first + 1) * n - 1) / W);
+        c1 = static_cast<int>(((first + nt) * n - 1) / W);
+    }
+    wait_for_prerequisites();
     if (blockIdx.x == 0) {
         for (int i = threadIdx.x; i < a.c.seqs; i += kThreads) clean_len(a, i, &bad);
         for (int i = threadIdx.x; i < a.ctas; i += kThreads) bad |= a.flags[i] != 0;
@@ -477,53 +517,73 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         if (threadIdx.x == 0 && lse != nullptr) *lse = -INFINITY;
         return;
     }
-    const int per_seq = a.c.heads_kv * a.chunks;
-    const int hk = head / a.group, g = head % a.group;
-    const int pair = hk * a.chunks + g / kPagedHeads, r = g % kPagedHeads;
-    const int64_t W = tiles * per_seq, first = front * per_seq + static_cast<int64_t>(pair) * nt;
-    // the CTA of unit u is the last one whose share begins at or before it
-    const int c0 = static_cast<int>(((first + 1) * a.ctas - 1) / W);
-    const int c1 = static_cast<int>(((first + nt) * a.ctas - 1) / W);
     if (c0 == c1) return;  // written whole
-    const float *ml = a.part + static_cast<int64_t>(2 * a.ctas) * kPagedHeads * D;
-    float mm = -INFINITY, ll = 0.f, o[kPer];
+    const int pieces = c1 - c0 + 1;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(2 * a.ctas) * kPagedHeads * D);
+    // piece p: the first one began in its CTA (slot 1), the others in an earlier one (slot 0)
+    auto slot_of = [&](int p) { return static_cast<int64_t>(2 * (c0 + p) + (p == 0 ? 1 : 0)) * kPagedHeads + r; };
+    float m[(kPagedCtas + kThreads - 1) / kThreads], l[(kPagedCtas + kThreads - 1) / kThreads], M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < (kPagedCtas + kThreads - 1) / kThreads; ++i) {
+        const int p = i * kThreads + threadIdx.x;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        if (p < pieces) {
+            const float2 v = ml[slot_of(p)];
+            m[i] = v.x;
+            l[i] = v.y;
+        }
+        M = fmaxf(M, m[i]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) part[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part[0][w]);
+    const float R = M == -INFINITY ? 0.f : M;
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < (kPagedCtas + kThreads - 1) / kThreads; ++i) {
+        const int p = i * kThreads + threadIdx.x;
+        const float w = fast_exp2(m[i] - R);
+        if (p < pieces) sw[p] = w;
+        total += w * l[i];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) part[1][warp] = total;
+    __syncthreads();
+    total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += part[1][w];
+    float o[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-    auto slot_of = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * kPagedHeads + r; };
-    for (int c = c0 + warp; c <= c1; c += kWarps) {
-        if (share(W, c, a.ctas) == share(W, c + 1, a.ctas)) continue;  // no share
-        mm = fmaxf(mm, ml[slot_of(c) * 2]);
-    }
-    const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-    for (int c = c0 + warp; c <= c1; c += kWarps) {
-        if (share(W, c, a.ctas) == share(W, c + 1, a.ctas)) continue;
-        const int64_t sl = slot_of(c);
-        const float w = fast_exp2(ml[sl * 2] - ref);
-        ll += w * ml[sl * 2 + 1];
-        const float *p = a.part + sl * D + lane * kPer;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] += w * p[e];
+#pragma unroll 8
+    for (int p = warp; p < pieces; p += kWarps) {
+        const float *src = a.part + slot_of(p) * D + lane * kPer;
+        const float w = sw[p];
+        if constexpr (kPer == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(src);
+            o[0] += w * v.x;
+            o[1] += w * v.y;
+            o[2] += w * v.z;
+            o[3] += w * v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(src);
+            o[0] += w * v.x;
+            o[1] += w * v.y;
+        }
     }
 #pragma unroll
     for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = o[e];
-    if (lane == 0) sml[warp][0] = mm, sml[warp][1] = ll;
     __syncthreads();
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w][0]);
-    const float R = M == -INFINITY ? 0.f : M;
-    float total = 0.f, f[kWarps];
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        f[w] = fast_exp2(sml[w][0] - R);
-        total += f[w] * sml[w][1];
-    }
     const float inv = total == 0.f ? 0.f : 1.f / total;
     for (int d = threadIdx.x; d < D; d += kThreads) {
         float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) x += f[w] * so[w][d];
+        for (int w = 0; w < kWarps; ++w) x += so[w][d];
         dst[d] = __float2bfloat16_rn(x * inv);
     }
     if (threadIdx.x == 0 && lse != nullptr)
@@ -552,8 +612,16 @@ static cudaError_t launch_paged(const nabla::PagedArgs &a, cudaStream_t stream) 
     paged_kernel<D><<<a.ctas, kThreads, smem_bytes<D>(), stream>>>(a);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    join_kernel<D><<<static_cast<unsigned>(a.c.seqs * a.heads), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.c.seqs * a.heads));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D>, a);
 }
 
 cudaError_t nabla_launch_paged(const nabla::PagedArgs &a, cudaStream_t stream) {
