@@ -15,7 +15,7 @@ cudaError_t nabla_launch_rope(nabla::RopeArgs &a, int dtype, int layout, int wid
                               cudaStream_t stream);
 cudaError_t nabla_launch_packed_fwd(const nabla::packed::Args &a, int D, cudaStream_t stream);
 cudaError_t nabla_launch_packed_bwd(const nabla::packed::Args &a, int D, int64_t q_tiles,
-                                    int64_t row_tiles, int64_t key_tiles, cudaStream_t stream);
+                                    int64_t key_tiles, cudaStream_t stream);
 cudaError_t nabla_launch_append(const nabla::AppendArgs &a, cudaStream_t stream);
 cudaError_t nabla_launch_paged(const nabla::PagedArgs &a, cudaStream_t stream);
 
@@ -415,7 +415,8 @@ int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const 
     if (row_tiles * shape->heads_kv > INT32_MAX || key_tiles * shape->heads_kv > INT32_MAX)
         return NABLA_ERR_SHAPE;
     cudaStream_t s = as_stream(stream);
-    if (cudaMemsetAsync(workspace, 0, sizeof(int), s) != cudaSuccess) return NABLA_ERR_CUDA;
+    // the status word and the unit counter behind it
+    if (cudaMemsetAsync(workspace, 0, 2 * sizeof(int), s) != cudaSuccess) return NABLA_ERR_CUDA;
     if (shape->total_q == 0 && shape->total_k == 0) return NABLA_OK;
     nabla::packed::Args a = packed_args(shape, cu_q, cu_k, workspace);
     a.q = dev_view(q);
@@ -428,10 +429,11 @@ int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const 
     a.dv = dev_view(dv);
     a.lse = const_cast<float *>(lse);
     a.pad_rows = q_tiles * 64;
+    a.units = row_tiles * shape->heads_kv;
     unsigned char *w = static_cast<unsigned char *>(workspace) + kStatusBytes;
     a.pad_l = reinterpret_cast<float *>(w);
     a.pad_d = reinterpret_cast<float *>(w + round256(sizeof(float) * a.pad_rows * shape->heads));
-    return cuda_status(nabla_launch_packed_bwd(a, shape->D, q_tiles, row_tiles, key_tiles, s));
+    return cuda_status(nabla_launch_packed_bwd(a, shape->D, q_tiles, key_tiles, s));
 }
 
 int nabla_cache_append(const nabla_cache *cache, const nabla_view *k, const nabla_view *v,

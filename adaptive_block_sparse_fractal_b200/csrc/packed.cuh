@@ -20,7 +20,7 @@ struct Args {
     View q, k, v, o, dout, dq, dk, dv;
     const int32_t *cu_q, *cu_k;
     float *lse;        // [heads, total_q]
-    int *status;       // workspace status word; behind it the forward's unit counter
+    int *status;       // workspace status word; behind it the unit counter
     float *pad_l, *pad_d;  // backward: [heads, pad_rows], -lse log2(e) and -dout.o
     float *part;       // split forward: partial rows, then their (m, l)
     int64_t total_q, total_k, pad_rows, units;  // units: upper bound of the forward's
@@ -108,21 +108,24 @@ __device__ __forceinline__ bool borders_ok(const Args &a) {
     return good;
 }
 
-// The next unit of a persistent launch (the counter starts at 0; the order in
-// which CTAs take units does not change what a unit computes).
+// The next unit of a persistent launch, whose CTAs begin with the unit of their
+// own index (the counter starts at 0; the order in which CTAs take units does not
+// change what a unit computes).
 __device__ __forceinline__ int64_t take_unit(const Args &a) {
-    return static_cast<int64_t>(atomicAdd(reinterpret_cast<unsigned int *>(a.status) + 1, 1u));
+    return static_cast<int64_t>(gridDim.x) + atomicAdd(reinterpret_cast<unsigned int *>(a.status) + 1, 1u);
 }
 
 // One warp's walk over the sequences for units that only grow: 32 sequences at
-// a time, their borders and running tile counts in registers.
+// a time, their borders and running tile counts in registers.  A sequence has
+// ceil(Lq * mul / len) tiles.
 struct UnitScan {
     int base, q0, q1, k0, k1;
     int64_t front, all;  // tiles in front of this lane's sequence and of the next 32
-    __device__ __forceinline__ UnitScan() : base(-32), q0(0), q1(0), k0(0), k1(0), front(0), all(0) {}
-    // sequence and tile (of `tile` tokens) of unit x; false behind the last
-    __device__ __forceinline__ bool find(const Args &a, int64_t x, int tile_len, int lane, int *oq0,
-                                         int *oLq, int *ok0, int *oLk, int *tile) {
+    int pad_front, pad_all;  // the same of 64-row tiles of q
+    __device__ __forceinline__ UnitScan()
+        : base(-32), q0(0), q1(0), k0(0), k1(0), front(0), all(0), pad_front(0), pad_all(0) {}
+    // sequence and tile of unit x; false behind the last
+    __device__ __forceinline__ bool find(const Args &a, int64_t x, int mul, int len, int lane, SeqTile *u) {
         while (x >= all) {
             base += 32;
             if (base >= a.seqs) {
@@ -137,27 +140,56 @@ struct UnitScan {
                 k0 = a.cu_k[s];
                 k1 = a.cu_k[s + 1];
             }
-            int64_t incl = (q1 - q0 + tile_len - 1) / tile_len;
-            const int64_t mine = incl;
+            const int64_t mine = ((q1 - q0) * mul + len - 1) / len;
+            const int pads = (q1 - q0 + 63) >> 6;
+            int64_t incl = mine;
+            int pincl = pads;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += t;
+                const int p = __shfl_up_sync(0xffffffffu, pincl, o);
+                if (lane >= o) {
+                    incl += t;
+                    pincl += p;
+                }
             }
             front = all + incl - mine;
+            pad_front = pad_all + pincl - pads;
             all += __shfl_sync(0xffffffffu, incl, 31);
+            pad_all += __shfl_sync(0xffffffffu, pincl, 31);
         }
         // the last lane whose sequence starts at or before x (empty ones share a start)
         const uint32_t at = __ballot_sync(0xffffffffu, front <= x);
         const int src = 31 - __clz(at);
-        *oq0 = __shfl_sync(0xffffffffu, q0, src);
-        *oLq = __shfl_sync(0xffffffffu, q1, src) - *oq0;
-        *ok0 = __shfl_sync(0xffffffffu, k0, src);
-        *oLk = __shfl_sync(0xffffffffu, k1, src) - *ok0;
-        *tile = static_cast<int>(x - __shfl_sync(0xffffffffu, front, src));
+        u->seq = base + src;
+        u->q0 = __shfl_sync(0xffffffffu, q0, src);
+        u->Lq = __shfl_sync(0xffffffffu, q1, src) - u->q0;
+        u->k0 = __shfl_sync(0xffffffffu, k0, src);
+        u->Lk = __shfl_sync(0xffffffffu, k1, src) - u->k0;
+        u->pad = __shfl_sync(0xffffffffu, pad_front, src);
+        u->tile = static_cast<int>(x - __shfl_sync(0xffffffffu, front, src));
         return true;
     }
 };
+
+// Rows of a warp's 32 threads -> global memory, 32 features of each: the rows
+// pass through 2 KB of shared memory, so that four lanes write 64 bytes of one
+// row (each thread storing its own row touches 32 rows an instruction and half
+// a sector of each).  `dst` is this lane's row, null where it is not written.
+__device__ __forceinline__ void store_rows(unsigned char *stage, const uint4 *w, __nv_bfloat16 *dst, int lane) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = w[c];
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int row = 8 * q + (lane >> 2), c = lane & 3;
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+        const uint64_t p = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), row);
+        if (p != 0) *(reinterpret_cast<uint4 *>(p) + c) = v;
+    }
+    __syncwarp();
+}
 
 // box of 64 features x one head x `rows` tokens
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint64_t *bar,

@@ -406,24 +406,36 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 // Thread (g, r) of the two dS warpgroups handles row r and keys [32 g, +32) of
 // the tile and writes their bf16 dS over its own S columns [32 g, +16).  Two
 // warps issue: warp 1 the S and dP MMAs, warp 10 the dQ MMAs.  With three S
-// buffers the S MMAs of tile t wait only for the dQ MMAs of tile t - 3, and
-// the one dP buffer is refilled once the dS warps hold tile t - 1's.
+// buffers the S MMAs of a tile wait only for the dQ MMAs of three tiles before,
+// and the one dP buffer is refilled once the dS warps hold the last tile's.
+// Persistent: a CTA takes units (128 rows) from a counter; the dS warps fetch
+// the next unit's Q and dO rows into registers in front of the last one's
+// epilogue, and K and V tiles of the next unit run ahead in the ring.  With
+// one CTA a unit, 8 key tiles a unit took 11 us each, most of it start and end.
 // TMEM columns: S(t) [64 (t % 3), +64), dP [192, 256), dQ [256, 256 + D),
 // Q [384, 384 + D/2), dO [448, 448 + D/2).
 constexpr int kDqThreads = 352;
 constexpr int kDqGradWarp = 10;
 constexpr uint32_t kDqColDP = 192, kColDQ = 256, kColQ = 384, kColDO = 448;
+
+// One unit, as the loading warp hands it to the others.
+struct DqUnit {
+    int valid, hk, q0, Lq, k0, Lk, pad;
+    int R0;  // first row
+    int nt;  // key tiles
+};
+
 template <int D>
 struct DqLayout {
     static constexpr int kHalves = D / 64;
     static constexpr int kDqRing = D == 128 ? 6 : 10;
     static constexpr uint32_t kBlockBytes = 64u * D * 2;  // 64 keys of K or V
     static constexpr uint32_t kDqSlot = 2 * kBlockBytes;
-    static constexpr uint32_t DQ_BAR = kDqRing * kDqSlot;
-    static constexpr int kBars = 2 * kDqRing + 3 + 3 + 1 + 1 + 3 + 1 + 1 + 1;
-    static constexpr uint32_t DQ_SEQ = DQ_BAR + 8 * kBars;
-    static constexpr uint32_t DQ_SUM = (DQ_SEQ + sizeof(SeqTile) + 7) / 8 * 8;
-    static constexpr uint32_t DQ_INT = DQ_SUM + 8 * (kDqThreads / 32);
+    static constexpr uint32_t DQ_STAGE = kDqRing * kDqSlot;  // 2 KB per dS warp
+    static constexpr uint32_t DQ_BAR = DQ_STAGE + 8 * 2048;
+    static constexpr int kBars = 2 * kDqRing + 3 + 3 + 1 + 1 + 3 + 1 + 1 + 1 + 4;
+    static constexpr uint32_t DQ_UNIT = DQ_BAR + 8 * kBars;
+    static constexpr uint32_t DQ_INT = (DQ_UNIT + 2 * sizeof(DqUnit) + 15) / 16 * 16;
     static constexpr uint32_t kSmem = DQ_INT + 16 + 1024;
 };
 
@@ -441,26 +453,17 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const uint32_t sRing = raw + pad;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::DQ_BAR);
     uint64_t *kv_full = bar, *kv_empty = bar + kDqRing, *s_full = bar + 2 * kDqRing;
-    // per S buffer t % 3: s_full (S(t), dP(t) complete), ds_full (the eight dS
-    // warps wrote dS(t)), s_free (the dQ MMAs of tile t read it)
+    // per S buffer: s_full (S, dP complete), ds_full (the eight dS warps wrote
+    // dS), s_free (the dQ MMAs have read it)
     uint64_t *ds_full = s_full + 3, *q_ready = ds_full + 3, *done = q_ready + 1;
     uint64_t *s_free = done + 1;
     uint64_t *dp_free = s_free + 3, *sdp_done = dp_free + 1, *raw_full = sdp_done + 1;
-    SeqTile *st = reinterpret_cast<SeqTile *>(sm + L::DQ_SEQ);
+    uint64_t *u_full = raw_full + 1, *u_empty = u_full + 2;  // per unit slot; read by ten warps
+    volatile DqUnit *units = reinterpret_cast<DqUnit *>(sm + L::DQ_UNIT);
     int *sInt = reinterpret_cast<int *>(sm + L::DQ_INT);  // [0] tmem base [2] abort
     volatile int *abort_flag = sInt + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int hk = static_cast<int>(blockIdx.x % a.heads_kv), G = a.group;
-    if (!find_seq<kDqThreads>(a, blockIdx.x / a.heads_kv, [=](int Lq, int) { return (Lq * G + 127) / 128; },
-                              st, reinterpret_cast<int64_t *>(sm + L::DQ_SUM)))
-        return;
-    const int Lq = st->Lq, Lk = st->Lk, off = Lk - Lq;
-    const int rows = Lq * G;  // below 2^31: heads * total_q is
-    // the last rows of a causal sequence keep the most keys: they go first
-    const int R0 = ((rows + 127) / 128 - 1 - st->tile) * 128;
-    const int last_tok = min(R0 + 127, rows - 1) / G;
-    const int kend = a.causal ? min(Lk, last_tok + 1 + off) : Lk;
-    const int nkeys = kend > 0 ? (kend + 63) >> 6 : 0;  // key tiles
+    const int G = a.group;
 
     if (threadIdx.x == 0) {
         for (int r = 0; r < kDqRing; ++r) {
@@ -477,6 +480,10 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         mbar_init(dp_free, 8);
         mbar_init(sdp_done, 1);
         mbar_init(raw_full, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&u_full[b], 1);
+            mbar_init(&u_empty[b], 10);
+        }
         sInt[2] = *reinterpret_cast<volatile int *>(a.status) != 0 ? 1 : 0;
         fence_mbar_init();
     }
@@ -484,82 +491,149 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         tmem_alloc(reinterpret_cast<uint32_t *>(&sInt[0]), 512);
         tmem_relinquish();
     }
+    const bool good = borders_ok(a);
     tc_fence_before();
-    __syncthreads();
+    const bool go = !__syncthreads_or(!good);
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(sInt[0]);
-    const int ntiles = nkeys;
+    bool ok = go && __all_sync(0xffffffffu, *abort_flag == 0);
 
     if (warp == 0) {
-        // ---------------- producer: K and V tiles through the ring ----------------
+        // ---------------- producer: units, then their K and V tiles through the ring ----------------
         if (lane == 0) {
             prefetch_tmap(&tk);
             prefetch_tmap(&tv);
         }
-        int t = 0;
-        for (; t < ntiles; ++t) {
-            const int slot = t % kDqRing;
-            const bool ok = __all_sync(
-                0xffffffffu, lane != 0 || wait_bar(&kv_empty[slot], ((t / kDqRing) & 1) ^ 1, abort_flag,
-                                                   a.status, a.limit));
-            if (!ok) break;
-            const uint32_t dst = sRing + slot * kDqSlot;
-            const int live = Lk - t * 64;
-            const bool zero = live < 64 && st->k0 + Lk < a.total_k;
-            uint64_t *full = zero ? raw_full : &kv_full[slot];
-            if (lane == 0) {
-                mbar_expect_tx(full, kDqSlot);
-                for (int h = 0; h < kHalves; ++h) {  // [K halves][V halves], 8 KB each
-                    tma_load_3d(dst + h * 8192, &tk, full, 64 * h, hk, st->k0 + t * 64);
-                    tma_load_3d(dst + kBlockBytes + h * 8192, &tv, full, 64 * h, hk, st->k0 + t * 64);
+        UnitScan scan;
+        int64_t x = blockIdx.x;
+        uint32_t seq = 0, tails = 0;
+        for (uint32_t n = 0; ok; ++n) {
+            const int us = n & 1;
+            DqUnit u = {};
+            x = __shfl_sync(0xffffffffu, x, 0);
+            const int64_t now = x;
+            if (now < a.units) {
+                if (lane == 0) x = take_unit(a);  // the next one, under this one's loads
+                SeqTile st;
+                u.hk = static_cast<int>(now % a.heads_kv);
+                u.valid = scan.find(a, now / a.heads_kv, G, 128, lane, &st);
+                if (u.valid) {
+                    u.q0 = st.q0;
+                    u.Lq = st.Lq;
+                    u.k0 = st.k0;
+                    u.Lk = st.Lk;
+                    u.pad = st.pad;
+                    const int rows = u.Lq * G;  // below 2^31: heads * total_q is
+                    // the last rows of a causal sequence keep the most keys: they go first
+                    u.R0 = ((rows + 127) / 128 - 1 - st.tile) * 128;
+                    const int last_tok = min(u.R0 + 127, rows - 1) / G;
+                    const int kend = a.causal ? min(u.Lk, last_tok + 1 + u.Lk - u.Lq) : u.Lk;
+                    u.nt = kend > 0 ? (kend + 63) >> 6 : 0;
                 }
             }
+            ok = __all_sync(0xffffffffu, lane != 0 || wait_bar(&u_empty[us], ((n >> 1) & 1u) ^ 1u, abort_flag,
+                                                               a.status, a.limit));
+            if (!ok) break;
+            if (lane == 0) {
+                volatile DqUnit &w = units[us];
+                w.valid = u.valid;
+                w.hk = u.hk;
+                w.q0 = u.q0;
+                w.Lq = u.Lq;
+                w.k0 = u.k0;
+                w.Lk = u.Lk;
+                w.pad = u.pad;
+                w.R0 = u.R0;
+                w.nt = u.nt;
+                mbar_arrive(&u_full[us]);
+            }
             __syncwarp();
-            if (zero) {  // at most once: the last tile
-                const bool in = wait_plain(raw_full, 0, a.limit);
-                if (!__all_sync(0xffffffffu, in)) break;
-                zero_rows(sm + slot * kDqSlot, live, 64, 2 * kHalves, 8192, lane);
-                if (lane == 0) mbar_arrive(&kv_full[slot]);
+            if (!u.valid) break;
+            for (int t = 0; ok && t < u.nt; ++t) {
+                const int slot = seq % kDqRing;
+                ok = __all_sync(0xffffffffu, lane != 0 || wait_bar(&kv_empty[slot], ((seq / kDqRing) & 1u) ^ 1u,
+                                                                   abort_flag, a.status, a.limit));
+                if (!ok) break;
+                const uint32_t dst = sRing + slot * kDqSlot;
+                const int live = u.Lk - t * 64;
+                const bool zero = live < 64 && u.k0 + u.Lk < a.total_k;
+                uint64_t *full = zero ? raw_full : &kv_full[slot];
+                if (lane == 0) {
+                    mbar_expect_tx(full, kDqSlot);
+                    for (int h = 0; h < kHalves; ++h) {  // [K halves][V halves], 8 KB each
+                        tma_load_3d(dst + h * 8192, &tk, full, 64 * h, u.hk, u.k0 + t * 64);
+                        tma_load_3d(dst + kBlockBytes + h * 8192, &tv, full, 64 * h, u.hk, u.k0 + t * 64);
+                    }
+                }
+                __syncwarp();
+                if (zero) {  // the last tile of a sequence
+                    ok = __all_sync(0xffffffffu, wait_plain(raw_full, tails++ & 1u, a.limit));
+                    if (!ok) break;
+                    zero_rows(sm + slot * kDqSlot, live, 64, 2 * kHalves, 8192, lane);
+                    if (lane == 0) mbar_arrive(&kv_full[slot]);
+                }
+                ++seq;
             }
         }
         // drain: never leave with a copy in flight
         if (lane == 0)
-            for (int u = t > kDqRing ? t - kDqRing : 0; u < t; ++u)
-                wait_plain(&kv_full[u % kDqRing], (u / kDqRing) & 1, a.limit);
+            for (uint32_t s = seq > kDqRing ? seq - kDqRing : 0; s < seq; ++s)
+                wait_plain(&kv_full[s % kDqRing], (s / kDqRing) & 1u, a.limit);
     } else if (warp == 1) {
         // ---------------- S / dP issuer (whole warp, one elected lane issues) ----------------
         constexpr uint32_t kIdS = idesc_bf16(128, 64, 0, 0);    // Q . K^T, dO . V^T
         auto off = [](int kk) { return static_cast<uint32_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4); };
-        bool ok = ntiles > 0 && warp_wait(q_ready, 0, abort_flag, a.status, a.limit);
-        for (int t = 0; ok && t < ntiles; ++t) {
-            const int slot = t % kDqRing, b = t % 3;
-            ok = warp_wait(&kv_full[slot], (t / kDqRing) & 1, abort_flag, a.status, a.limit);
-            // S buffer t % 3 is free once the dQ MMAs of tile t - 3 have read its dS
-            if (ok && t >= 3)
-                ok = warp_wait(&s_free[b], ((t / 3) - 1) & 1, abort_flag, a.status, a.limit);
+        int slot = 0, b = 0;
+        uint32_t kv_phase = 0, turn = 0, loaded = 0;  // turn: uses of the S buffers / 3; loaded: units with keys
+        uint32_t tiles = 0;
+        for (uint32_t n = 0; ok; ++n) {
+            const int us = n & 1;
+            ok = warp_wait(&u_full[us], (n >> 1) & 1u, abort_flag, a.status, a.limit);
             if (!ok) break;
-            tc_fence_after();
-            const uint32_t b0 = sRing + slot * kDqSlot;
-            const uint32_t d = tmem + 64 * b;
-            // descriptors advance by (byte offset >> 4) in their low address field
-            const uint64_t dK = desc_sw128(b0, 16, 1024), dV = desc_sw128(b0 + kBlockBytes, 16, 1024);
-            // S first ...
+            const int valid = units[us].valid, nt = units[us].nt;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&u_empty[us]);
+            if (!valid) break;
+            if (nt == 0) continue;
+            ok = warp_wait(q_ready, loaded++ & 1u, abort_flag, a.status, a.limit);
+            for (int t = 0; ok && t < nt; ++t, ++tiles) {
+                ok = warp_wait(&kv_full[slot], kv_phase, abort_flag, a.status, a.limit);
+                // an S buffer is free once the dQ MMAs of its last tile have read its dS
+                if (ok && turn > 0) ok = warp_wait(&s_free[b], (turn - 1) & 1u, abort_flag, a.status, a.limit);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t b0 = sRing + slot * kDqSlot;
+                const uint32_t d = tmem + 64 * b;
+                // descriptors advance by (byte offset >> 4) in their low address field
+                const uint64_t dK = desc_sw128(b0, 16, 1024), dV = desc_sw128(b0 + kBlockBytes, 16, 1024);
+                // S first ...
 #pragma unroll
-            for (int kk = 0; kk < D / 16; kk += 4)
-                mma_ts4_warp(d, d, d, d, tmem + kColQ + 8 * kk, tmem + kColQ + 8 * kk + 8,
-                             tmem + kColQ + 8 * kk + 16, tmem + kColQ + 8 * kk + 24, dK + off(kk),
-                             dK + off(kk + 1), dK + off(kk + 2), dK + off(kk + 3), kIdS, kk > 0, 1u);
-            // ... then dP into the single buffer, once the dS warps hold tile
-            // t - 1's in registers
-            if (t > 0 && !warp_wait(dp_free, (t - 1) & 1, abort_flag, a.status, a.limit)) break;
-            tc_fence_after();
+                for (int kk = 0; kk < D / 16; kk += 4)
+                    mma_ts4_warp(d, d, d, d, tmem + kColQ + 8 * kk, tmem + kColQ + 8 * kk + 8,
+                                 tmem + kColQ + 8 * kk + 16, tmem + kColQ + 8 * kk + 24, dK + off(kk),
+                                 dK + off(kk + 1), dK + off(kk + 2), dK + off(kk + 3), kIdS, kk > 0, 1u);
+                // ... then dP into the single buffer, once the dS warps hold the last tile's
+                if (tiles > 0 && !warp_wait(dp_free, (tiles - 1) & 1u, abort_flag, a.status, a.limit)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < D / 16; kk += 4)
-                mma_ts4_warp(tmem + kDqColDP, tmem + kDqColDP, tmem + kDqColDP, tmem + kDqColDP,
-                             tmem + kColDO + 8 * kk, tmem + kColDO + 8 * kk + 8, tmem + kColDO + 8 * kk + 16,
-                             tmem + kColDO + 8 * kk + 24, dV + off(kk), dV + off(kk + 1), dV + off(kk + 2),
-                             dV + off(kk + 3), kIdS, kk > 0, 1u);
-            mma_commit_warp(&s_full[b]);
+                for (int kk = 0; kk < D / 16; kk += 4)
+                    mma_ts4_warp(tmem + kDqColDP, tmem + kDqColDP, tmem + kDqColDP, tmem + kDqColDP,
+                                 tmem + kColDO + 8 * kk, tmem + kColDO + 8 * kk + 8, tmem + kColDO + 8 * kk + 16,
+                                 tmem + kColDO + 8 * kk + 24, dV + off(kk), dV + off(kk + 1), dV + off(kk + 2),
+                                 dV + off(kk + 3), kIdS, kk > 0, 1u);
+                mma_commit_warp(&s_full[b]);
+                if (++slot == kDqRing) {
+                    slot = 0;
+                    kv_phase ^= 1u;
+                }
+                if (++b == 3) {
+                    b = 0;
+                    ++turn;
+                }
+            }
         }
         mma_commit_warp(sdp_done);  // completes once every MMA issued above has finished
         if (lane == 0) wait_plain(sdp_done, 0, a.limit);
@@ -567,21 +641,45 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     } else if (warp == kDqGradWarp) {
         // ---------------- dQ issuer (whole warp, one elected lane issues) ----------------
         constexpr uint32_t kIdQ = idesc_bf16(128, D, 0, 1);     // dS . K (K MN-major)
-        for (int t = 0; t < ntiles; ++t) {
-            const int slot = t % kDqRing, b = t % 3;
-            if (!warp_wait(&ds_full[b], (t / 3) & 1, abort_flag, a.status, a.limit)) break;
-            tc_fence_after();
-            // K as the MN-major B operand: key k-step kk starts 2048 bytes further
-            // and reads bf16 dS columns 32 (kk / 2) + 8 (kk % 2) of this tile's S
-            const uint64_t gK = desc_sw128(sRing + slot * kDqSlot, 8192, 1024);
-            const uint32_t c = tmem + 64 * b;
-            mma_ts4_warp(tmem + kColDQ, tmem + kColDQ, tmem + kColDQ, tmem + kColDQ, c, c + 8, c + 32,
-                         c + 40, gK, gK + 128, gK + 256, gK + 384, kIdQ, t > 0 ? 1u : 0u, 1u);
-            mma_commit_warp(&kv_empty[slot]);
-            mma_commit_warp(&s_free[b]);
+        int slot = 0, b = 0;
+        uint32_t phase = 0, ended = 0;
+        for (uint32_t n = 0; ok; ++n) {
+            const int us = n & 1;
+            ok = warp_wait(&u_full[us], (n >> 1) & 1u, abort_flag, a.status, a.limit);
+            if (!ok) break;
+            const int valid = units[us].valid, nt = units[us].nt;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&u_empty[us]);
+            if (!valid) break;
+            if (nt == 0) continue;
+            for (int t = 0; ok && t < nt; ++t) {
+                ok = warp_wait(&ds_full[b], phase, abort_flag, a.status, a.limit);
+                if (!ok) break;
+                tc_fence_after();
+                // K as the MN-major B operand: key k-step kk starts 2048 bytes further
+                // and reads bf16 dS columns 32 (kk / 2) + 8 (kk % 2) of this tile's S
+                const uint64_t gK = desc_sw128(sRing + slot * kDqSlot, 8192, 1024);
+                const uint32_t c = tmem + 64 * b;
+                mma_ts4_warp(tmem + kColDQ, tmem + kColDQ, tmem + kColDQ, tmem + kColDQ, c, c + 8, c + 32,
+                             c + 40, gK, gK + 128, gK + 256, gK + 384, kIdQ, t > 0 ? 1u : 0u, 1u);
+                mma_commit_warp(&kv_empty[slot]);
+                mma_commit_warp(&s_free[b]);
+                if (++slot == kDqRing) slot = 0;
+                if (++b == 3) {
+                    b = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (ok) {
+                mma_commit_warp(done);  // the unit's dQ is complete
+                ++ended;
+            }
         }
-        mma_commit_warp(done);  // completes once every MMA issued above has finished
-        if (lane == 0) wait_plain(done, 0, a.limit);
+        if (!ok) {  // given up inside a unit: its MMAs still have to finish
+            mma_commit_warp(done);
+            ++ended;
+        }
+        if (lane == 0 && ended > 0) wait_plain(done, (ended - 1) & 1u, a.limit);
         __syncwarp();
     } else {
         // ---------------- dS warpgroups: row r, key half kg ----------------
@@ -589,103 +687,135 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         const int kg = (warp - 2) >> 2;             // 0: keys 0-31, 1: keys 32-63
         const int r = wq * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-        const bool real = R0 + r < rows;
-        const int row = min(R0 + r, rows - 1);
-        const int tok = row / G, head = hk * G + row % G;
-        const int64_t prow = head * a.pad_rows + static_cast<int64_t>(st->pad) * 64 + tok;
-        const float nLr = a.pad_l[prow], nDr = a.pad_d[prow];
-        bool ok = true;
-        {
-            // Q (group 0) or dO (group 1) row -> TMEM, the A operands of S and dP
-            const uint4 *src = reinterpret_cast<const uint4 *>((kg ? a.dout : a.q).row(st->q0 + tok, head));
-            const uint32_t col = kg ? kColDO : kColQ;
+        unsigned char *stage = sm + L::DQ_STAGE + (warp - 2) * 2048;
+        const uint64_t c2 = f2_pack(a.c, a.c);
+        uint32_t v32[D / 2];  // the next unit's Q row (group 0) or dO row (group 1)
+        float nLr = 0.f, nDr = 0.f;
+        // row of the unit in slot us: token and head, clamped to a real one
+        auto place = [&](int us, int *tok, int *head) -> bool {
+            const int rows = units[us].Lq * G, R0 = units[us].R0;
+            const int row = min(R0 + r, rows - 1);
+            *tok = row / G;
+            *head = units[us].hk * G + row % G;
+            return R0 + r < rows;
+        };
+        auto fetch = [&](int us) {
+            int tok, head;
+            place(us, &tok, &head);
+            const int64_t prow = head * a.pad_rows + static_cast<int64_t>(units[us].pad) * 64 + tok;
+            nLr = a.pad_l[prow];
+            nDr = a.pad_d[prow];
+            const uint4 *src = reinterpret_cast<const uint4 *>((kg ? a.dout : a.q).row(units[us].q0 + tok, head));
 #pragma unroll
-            for (int half = 0; half < D / 64; ++half) {
-                uint32_t v32[32];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint4 v = __ldg(src + 8 * half + e);
-                    v32[4 * e] = v.x;
-                    v32[4 * e + 1] = v.y;
-                    v32[4 * e + 2] = v.z;
-                    v32[4 * e + 3] = v.w;
-                }
-                tmem_st32(tmem + lane_base + col + 32 * half, reinterpret_cast<float *>(v32));
+            for (int e = 0; e < D / 8; ++e) {
+                const uint4 v = __ldg(src + e);
+                v32[4 * e] = v.x;
+                v32[4 * e + 1] = v.y;
+                v32[4 * e + 2] = v.z;
+                v32[4 * e + 3] = v.w;
             }
-            tmem_wait_st();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_ready);
-        const int lim = a.causal ? min(Lk - 1, tok + off) : Lk - 1;  // last key of this row
-        const int lim0 = a.causal ? min(Lk - 1, R0 / G + off) : Lk - 1;
-        const uint64_t c2 = f2_pack(a.c, a.c), nl2 = f2_pack(nLr, nLr), nd2 = f2_pack(nDr, nDr);
-        const int nt = *abort_flag ? 0 : ntiles;
-        for (int t = 0; t < nt; ++t) {
-            ok = wait_bar(&s_full[t % 3], (t / 3) & 1, abort_flag, a.status, a.limit) && ok;
+        };
+        auto arrived = [&](uint32_t n) -> bool {  // the unit's description
+            return __all_sync(0xffffffffu, wait_bar(&u_full[n & 1], (n >> 1) & 1u, abort_flag, a.status, a.limit));
+        };
+        int b = 0;
+        uint32_t phase = 0, ended = 0;
+        ok = ok && arrived(0);
+        if (ok && units[0].valid && units[0].nt > 0) fetch(0);
+        for (uint32_t n = 0; ok; ++n) {
+            const int us = n & 1;
+            if (!units[us].valid) break;
+            const int nt = units[us].nt;
+            const uint64_t nl2 = f2_pack(nLr, nLr), nd2 = f2_pack(nDr, nDr);
+            int tok, head;
+            const bool real = place(us, &tok, &head);
+            const int64_t grow = units[us].q0 + tok;
+            const int Lk = units[us].Lk, shift = Lk - units[us].Lq;
+            int left = (a.causal ? min(Lk - 1, tok + shift) : Lk - 1) - 32 * kg;  // last key of this row
+            int left0 = a.causal ? min(Lk - 1, units[us].R0 / G + shift) : Lk - 1;  // of the first row
+            if (nt > 0) {
+                // A operands of S and dP (the MMAs of the unit before have finished)
+                const uint32_t col = kg ? kColDO : kColQ;
+#pragma unroll
+                for (int half = 0; half < D / 64; ++half)
+                    tmem_st32(tmem + lane_base + col + 32 * half, reinterpret_cast<float *>(v32 + 32 * half));
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_ready);
+            }
+            for (int t = 0; t < nt; ++t, left -= 64, left0 -= 64) {
+                ok = wait_bar(&s_full[b], phase, abort_flag, a.status, a.limit) && ok;
+                tc_fence_after();
+                const uint32_t scol = tmem + lane_base + b * 64 + 32 * kg;
+                uint32_t gk[16];
+                float sv[32], dp[32];
+                tmem_ld32(scol, sv);
+                tmem_ld32(tmem + lane_base + kDqColDP + 32 * kg, dp);
+                tmem_wait_ld();
+                // dP is in registers: the buffer may take the next tile's
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dp_free);
+                if (63 > left0) {  // masked tile: P = 0 and no NaN out of dP
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        sv[e] = e <= left ? sv[e] : -INFINITY;
+                        dp[e] = e <= left ? dp[e] : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const uint64_t x = f2_fma(f2_pack(sv[e], sv[e + 1]), c2, nl2);
+                    const uint64_t g = f2_mul(f2_pack(fast_exp2(f2_lo(x)), fast_exp2(f2_hi(x))),
+                                              f2_add(f2_pack(dp[e], dp[e + 1]), nd2));
+                    gk[e >> 1] = pack_bf16(f2_lo(g), f2_hi(g));
+                }
+                // bf16 dS of keys [32 kg, 32 kg + 32) over this group's first 16 S columns
+                tmem_st16(scol, gk);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ds_full[b]);
+                if (++b == 3) {
+                    b = 0;
+                    phase ^= 1u;
+                }
+            }
+            // the next unit's rows travel while this one ends
+            ok = ok && arrived(n + 1);
+            ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+            if (!ok) break;
+            if (units[us ^ 1].valid && units[us ^ 1].nt > 0) fetch(us ^ 1);
+            // ---------------- epilogue: group kg writes dQ features [D/2 kg, +D/2) ----------------
+            if (nt > 0) ok = wait_bar(done, ended++ & 1u, abort_flag, a.status, a.limit);
             tc_fence_after();
-            const uint32_t scol = tmem + lane_base + (t % 3) * 64 + 32 * kg;
-            uint32_t gk[16];
-            float sv[32], dp[32];
-            tmem_ld32(scol, sv);
-            tmem_ld32(tmem + lane_base + kDqColDP + 32 * kg, dp);
-            tmem_wait_ld();
-            // dP is in registers: the buffer may take the next tile's
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dp_free);
-            if (t * 64 + 63 > lim0) {  // masked tile: P = 0 and no NaN out of dP
-                const int left = lim - t * 64 - 32 * kg;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    sv[e] = e <= left ? sv[e] : -INFINITY;
-                    dp[e] = e <= left ? dp[e] : 0.f;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const uint64_t x = f2_fma(f2_pack(sv[e], sv[e + 1]), c2, nl2);
-                const uint64_t g = f2_mul(f2_pack(fast_exp2(f2_lo(x)), fast_exp2(f2_hi(x))),
-                                          f2_add(f2_pack(dp[e], dp[e + 1]), nd2));
-                gk[e >> 1] = pack_bf16(f2_lo(g), f2_hi(g));
-            }
-            // bf16 dS of keys [32 kg, 32 kg + 32) over this group's first 16 S columns
-            tmem_st16(scol, gk);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ds_full[t % 3]);
-        }
-        // ---------------- epilogue: group kg writes dQ features [D/2 kg, +D/2) ----------------
-        if (ok && nt > 0) ok = wait_bar(done, 0, abort_flag, a.status, a.limit);
-        tc_fence_after();
-        // warp-uniform flags around the collective TMEM loads
-        const bool aborted = __any_sync(0xffffffffu, *abort_flag != 0);
-        const bool live = !aborted && nt > 0 && __all_sync(0xffffffffu, ok);
-        if (!aborted) {
-            __nv_bfloat16 *dst = a.dq.row(st->q0 + tok, head) + (D / 2) * kg;
+            ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+            if (!ok) break;
+            __nv_bfloat16 *dst = real ? a.dq.row(grow, head) + (D / 2) * kg : nullptr;
 #pragma unroll
             for (int part = 0; part < D / 64; ++part) {
                 float v[32];
-                if (live) {
+                if (nt > 0) {
                     tmem_ld32(tmem + lane_base + kColDQ + (D / 2) * kg + 32 * part, v);
                     tmem_wait_ld();
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.f;
                 }
-                if (real) {
+                uint4 w[4];
 #pragma unroll
-                    for (int e8 = 0; e8 < 4; ++e8) {
-                        uint4 w;
-                        w.x = pack_bf16(v[8 * e8] * a.scale, v[8 * e8 + 1] * a.scale);
-                        w.y = pack_bf16(v[8 * e8 + 2] * a.scale, v[8 * e8 + 3] * a.scale);
-                        w.z = pack_bf16(v[8 * e8 + 4] * a.scale, v[8 * e8 + 5] * a.scale);
-                        w.w = pack_bf16(v[8 * e8 + 6] * a.scale, v[8 * e8 + 7] * a.scale);
-                        *reinterpret_cast<uint4 *>(dst + 32 * part + 8 * e8) = w;
-                    }
+                for (int e8 = 0; e8 < 4; ++e8) {
+                    w[e8].x = pack_bf16(v[8 * e8] * a.scale, v[8 * e8 + 1] * a.scale);
+                    w[e8].y = pack_bf16(v[8 * e8 + 2] * a.scale, v[8 * e8 + 3] * a.scale);
+                    w[e8].z = pack_bf16(v[8 * e8 + 4] * a.scale, v[8 * e8 + 5] * a.scale);
+                    w[e8].w = pack_bf16(v[8 * e8 + 6] * a.scale, v[8 * e8 + 7] * a.scale);
                 }
+                store_rows(stage, w, dst == nullptr ? nullptr : dst + 32 * part, lane);
             }
+            tc_fence_before();  // dQ is read: the next unit's first dQ MMA may overwrite it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&u_empty[us]);
         }
     }
     tc_fence_before();
@@ -698,12 +828,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 }  // namespace nabla
 
 template <int D>
-static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_tiles, int64_t row_tiles,
-                                     int64_t key_tiles, cudaStream_t stream) {
+static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_tiles, int64_t key_tiles,
+                                     cudaStream_t stream) {
     using namespace nabla::packed;
     cudaError_t err;
     if (a.total_q > 0) {
-        const int per = 8;  // heads a CTA of pre_kernel
+        const int per = 1;  // heads a CTA of pre_kernel
         pre_kernel<D><<<dim3(static_cast<unsigned>(q_tiles), (a.heads + per - 1) / per), kPreThreads, 0,
                         stream>>>(a, per);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
@@ -732,16 +862,16 @@ static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_til
         err = cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(kSmem));
         if (err != cudaSuccess) return err;
-        dq_kernel<D><<<static_cast<unsigned>(row_tiles * a.heads_kv), kDqThreads, kSmem, stream>>>(mk, mv, a);
+        dq_kernel<D><<<static_cast<unsigned>(a.units < kSms ? a.units : kSms), kDqThreads, kSmem, stream>>>(mk, mv, a);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
     return cudaSuccess;
 }
 
-// Upper bounds over the sequences: 64-row tiles of q, 128-row tiles of the
-// (token, head of a group) rows, 128-key tiles
+// Upper bounds over the sequences: 64-row tiles of q, 128-key tiles (and, in
+// a.units, 128-row tiles of the (token, head of a group) rows x heads_kv)
 cudaError_t nabla_launch_packed_bwd(const nabla::packed::Args &a, int D, int64_t q_tiles,
-                                    int64_t row_tiles, int64_t key_tiles, cudaStream_t stream) {
-    return D == 128 ? launch_packed_bwd<128>(a, q_tiles, row_tiles, key_tiles, stream)
-                    : launch_packed_bwd<64>(a, q_tiles, row_tiles, key_tiles, stream);
+                                    int64_t key_tiles, cudaStream_t stream) {
+    return D == 128 ? launch_packed_bwd<128>(a, q_tiles, key_tiles, stream)
+                    : launch_packed_bwd<64>(a, q_tiles, key_tiles, stream);
 }

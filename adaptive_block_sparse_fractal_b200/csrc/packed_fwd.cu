@@ -89,16 +89,17 @@ struct Unit {
 template <int D>
 struct FwdLayout {
     static constexpr int kHalves = D / 64;
-    static constexpr int kRing = D == 128 ? 5 : 9;
+    static constexpr int kRing = D == 128 ? 4 : 8;  // K and V tiles in flight (5 at D = 128 were no faster)
     static constexpr uint32_t kTile = 128u * D * 2;  // 128 rows x D bf16
     static constexpr uint32_t OFF_Q = 0;             // two row tiles
     static constexpr uint32_t OFF_RING = 2 * kTile;
-    static constexpr uint32_t OFF_BAR = OFF_RING + kRing * kTile;
+    static constexpr uint32_t OFF_STAGE = OFF_RING + kRing * kTile;  // 2 KB per softmax warp
+    static constexpr uint32_t OFF_BAR = OFF_STAGE + 16 * 2048;
     static constexpr int kBars = 2 * kRing + 4 + 2 + 4 + 2 + 4 + 1 + 4;
     static constexpr uint32_t OFF_UNIT = OFF_BAR + 8 * kBars;
     static constexpr uint32_t OFF_RED = (OFF_UNIT + 2 * sizeof(Unit) + 15) / 16 * 16;  // maxima or sums: [tile][half][row]
     static constexpr uint32_t OFF_INT = OFF_RED + 2 * 2 * 128 * 4;
-    static constexpr uint32_t kSmem = OFF_INT + 16;  // no room for an alignment pad at D = 128
+    static constexpr uint32_t kSmem = OFF_INT + 16;  // (no alignment pad: aligned as declared)
 };
 
 // 2^x of a pair on the SFU
@@ -255,14 +256,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     x = __shfl_sync(0xffffffffu, x, 0);
                     const int64_t now = x;
                     if (now < a.units) {
-                        if (lane == 0) x = take_unit(a) + gridDim.x;  // the next one, under this one's loads
+                        if (lane == 0) x = take_unit(a);  // the next one, under this one's loads
                         const int64_t ux = now / a.splits;
-                        int tile = 0;
+                        SeqTile st;
                         u.split = static_cast<int>(now % a.splits);
                         u.hk = static_cast<int>(ux % a.heads_kv);
-                        u.valid = scan.find(a, ux / a.heads_kv, 2 * tpt, lane, &u.q0, &u.Lq, &u.k0, &u.Lk, &tile);
-                        // the last tiles of a causal sequence keep the most keys: they go first
-                        if (u.valid) u.tok0 = ((u.Lq + 2 * tpt - 1) / (2 * tpt) - 1 - tile) * 2 * tpt;
+                        u.valid = scan.find(a, ux / a.heads_kv, 1, 2 * tpt, lane, &st);
+                        if (u.valid) {
+                            u.q0 = st.q0;
+                            u.Lq = st.Lq;
+                            u.k0 = st.k0;
+                            u.Lk = st.Lk;
+                            // the last tiles of a causal sequence keep the most keys: they go first
+                            u.tok0 = ((u.Lq + 2 * tpt - 1) / (2 * tpt) - 1 - st.tile) * 2 * tpt;
+                        }
                     }
                     if (!u.valid && n >= 1) {  // the end, unless the other slot's unit has to be taken again
                         ok = __all_sync(0xffffffffu, lane != 0 || wait_bar(&u_empty[us ^ 1], ((n - 1) >> 1) & 1u,
@@ -618,7 +625,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (h == 0 && real && a.lse != nullptr)
                     a.lse[head * a.total_q + grow] = l > 0.f ? (m + log2f(l)) * kFwdLn2 : l == 0.f ? -INFINITY : l;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                __nv_bfloat16 *dst = a.o.row(grow, head) + (D / 2) * h;
+                __nv_bfloat16 *dst = real ? a.o.row(grow, head) + (D / 2) * h : nullptr;
+                unsigned char *stage = sm + L::OFF_STAGE + (warp - 4) * 2048;
 #pragma unroll
                 for (int part = 0; part < D / 64; ++part) {
                     float ov[32];
@@ -630,17 +638,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                         for (int q = 0; q < 32; ++q) ov[q] = 0.f;
                     }
-                    if (real) {
+                    uint4 w[4];
 #pragma unroll
-                        for (int e8 = 0; e8 < 4; ++e8) {
-                            uint4 w;
-                            w.x = pack_bf16(ov[8 * e8] * inv, ov[8 * e8 + 1] * inv);
-                            w.y = pack_bf16(ov[8 * e8 + 2] * inv, ov[8 * e8 + 3] * inv);
-                            w.z = pack_bf16(ov[8 * e8 + 4] * inv, ov[8 * e8 + 5] * inv);
-                            w.w = pack_bf16(ov[8 * e8 + 6] * inv, ov[8 * e8 + 7] * inv);
-                            *reinterpret_cast<uint4 *>(dst + 32 * part + 8 * e8) = w;
-                        }
+                    for (int e8 = 0; e8 < 4; ++e8) {
+                        w[e8].x = pack_bf16(ov[8 * e8] * inv, ov[8 * e8 + 1] * inv);
+                        w[e8].y = pack_bf16(ov[8 * e8 + 2] * inv, ov[8 * e8 + 3] * inv);
+                        w[e8].z = pack_bf16(ov[8 * e8 + 4] * inv, ov[8 * e8 + 5] * inv);
+                        w[e8].w = pack_bf16(ov[8 * e8 + 6] * inv, ov[8 * e8 + 7] * inv);
                     }
+                    store_rows(stage, w, dst == nullptr ? nullptr : dst + 32 * part, lane);
                 }
             } else {
                 // unnormalised part of this split: [split][token][head][D], then (m, l)
