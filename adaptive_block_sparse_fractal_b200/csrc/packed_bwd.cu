@@ -41,6 +41,7 @@ template <int D>
 __global__ void __launch_bounds__(kPreThreads) pre_kernel(const __grid_constant__ Args a, int per) {
     __shared__ SeqTile st;
     __shared__ int64_t sums[kPreThreads / 32];
+    allow_dependents();
     if (!find_seq<kPreThreads>(a, blockIdx.x, [](int Lq, int) { return (Lq + 63) >> 6; }, &st, sums))
         return;
     constexpr int TPR = D / 8;  // threads per row, 8 features each
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     const int hk = static_cast<int>(blockIdx.x % a.heads_kv);
     if (!find_seq<kKvThreads>(a, blockIdx.x / a.heads_kv, [](int, int Lk) { return (Lk + 127) >> 7; }, st,
                               reinterpret_cast<int64_t *>(sm + L::KV_SUM)))
-        return;
+        return;  // (an exit counts as both of the calls below)
     const int Lq = st->Lq, Lk = st->Lk, off = Lk - Lq, G = a.group;
     const int j0 = st->tile * 128;  // first key
     // query tiles [qs, qs + per) of each head: query i keeps keys up to i + off
@@ -162,6 +163,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(sInt[0]);
     const int ntiles = G * per;
+    // pre_kernel has finished from here on; then dQ's CTAs may take the SMs that
+    // this launch leaves idle (they read nothing that it writes)
+    wait_for_prerequisites();
+    allow_dependents();
 
     if (warp == 0) {
         // ---------------- producer: V once, then the query stages ----------------
@@ -822,6 +827,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+    wait_for_prerequisites();  // the end of this launch is the end of the dK, dV one too
 }
 
 }  // namespace packed
@@ -833,7 +839,7 @@ static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_til
     using namespace nabla::packed;
     cudaError_t err;
     if (a.total_q > 0) {
-        const int per = 1;  // heads a CTA of pre_kernel
+        const int per = 2;  // heads a CTA of pre_kernel: 24 us at 100 MB; 8 a CTA took 38
         pre_kernel<D><<<dim3(static_cast<unsigned>(q_tiles), (a.heads + per - 1) / per), kPreThreads, 0,
                         stream>>>(a, per);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
@@ -853,17 +859,20 @@ static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_til
         err = cudaFuncSetAttribute(dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(kSmem));
         if (err != cudaSuccess) return err;
-        dkdv_kernel<D><<<static_cast<unsigned>(key_tiles * a.heads_kv), kKvThreads, kSmem, stream>>>(
-            mq, mv128, mdo, a);
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+        err = nabla_launch_early(dkdv_kernel<D>, static_cast<unsigned>(key_tiles * a.heads_kv), kKvThreads, kSmem,
+                                 stream, mq, mv128, mdo, a);
+        if (err != cudaSuccess) return err;
     }
     if (q) {
         constexpr uint32_t kSmem = DqLayout<D>::kSmem;
         err = cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(kSmem));
         if (err != cudaSuccess) return err;
-        dq_kernel<D><<<static_cast<unsigned>(a.units < kSms ? a.units : kSms), kDqThreads, kSmem, stream>>>(mk, mv, a);
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+        const unsigned grid = static_cast<unsigned>(a.units < kSms ? a.units : kSms);
+        if (k)
+            return nabla_launch_early(dq_kernel<D>, grid, kDqThreads, kSmem, stream, mk, mv, a);
+        dq_kernel<D><<<grid, kDqThreads, kSmem, stream>>>(mk, mv, a);
+        return cudaGetLastError();
     }
     return cudaSuccess;
 }
