@@ -364,8 +364,10 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
     const int splits = fwd_splits(shape);
     if (units > INT32_MAX / splits) return NABLA_ERR_SHAPE;
     cudaStream_t s = as_stream(stream);
-    // the status word and the unit counter behind it
-    if (cudaMemsetAsync(workspace, 0, 2 * sizeof(int), s) != cudaSuccess) return NABLA_ERR_CUDA;
+    // the status word and the unit counter behind it; with no more units than
+    // CTAs the counter is not used, and the kernel writes the status itself
+    if (shape->total_q == 0 || units * splits > nabla::packed::kSms)
+        if (cudaMemsetAsync(workspace, 0, 2 * sizeof(int), s) != cudaSuccess) return NABLA_ERR_CUDA;
     if (shape->total_q == 0) return NABLA_OK;
     nabla::packed::Args a = packed_args(shape, cu_q, cu_k, workspace);
     a.q = dev_view(q);

@@ -3,6 +3,7 @@
 // tensor maps over strided [tokens, heads, D] views.
 #pragma once
 
+#include "launch.cuh"
 #include "sm100.cuh"
 
 namespace nabla {
@@ -225,14 +226,6 @@ __device__ __forceinline__ void tmem_wait_ld_of(float *v) {
                  : "memory");
 }
 
-// Programmatic dependent launch.
-__device__ __forceinline__ void allow_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_prerequisites() {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-}
-
 // Register share of a warpgroup (all four of its warps execute it).
 template <int N>
 __device__ __forceinline__ void reg_alloc() {
@@ -257,23 +250,6 @@ __device__ __forceinline__ void zero_rows(unsigned char *tile, int from, int row
 
 }  // namespace packed
 }  // namespace nabla
-
-// Host: a launch that may start while its predecessor in the stream still runs.
-template <typename... P, typename... A>
-inline cudaError_t nabla_launch_early(void (*kernel)(P...), unsigned grid, unsigned block, uint32_t smem,
-                                      cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 // Host: tensor map over a [tokens, heads, D] bf16 view, boxes of 64 features x
 // box_heads heads x `rows` tokens, 128-byte swizzle (defined in packed_fwd.cu).

@@ -856,8 +856,7 @@ static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_til
         return cudaErrorInvalidValue;
     if (k) {
         constexpr uint32_t kSmem = KvLayout<D>::kSmem;
-        err = cudaFuncSetAttribute(dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(kSmem));
+        err = nabla_allow_smem<dkdv_kernel<D>>(kSmem);
         if (err != cudaSuccess) return err;
         err = nabla_launch_early(dkdv_kernel<D>, static_cast<unsigned>(key_tiles * a.heads_kv), kKvThreads, kSmem,
                                  stream, mq, mv128, mdo, a);
@@ -865,8 +864,7 @@ static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_til
     }
     if (q) {
         constexpr uint32_t kSmem = DqLayout<D>::kSmem;
-        err = cudaFuncSetAttribute(dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(kSmem));
+        err = nabla_allow_smem<dq_kernel<D>>(kSmem);
         if (err != cudaSuccess) return err;
         const unsigned grid = static_cast<unsigned>(a.units < kSms ? a.units : kSms);
         if (k)

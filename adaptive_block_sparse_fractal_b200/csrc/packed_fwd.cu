@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(&u_empty[t], 18);
         }
         mbar_init(raw_full, 1);
-        sInt[2] = *reinterpret_cast<volatile int *>(a.status) != 0 ? 1 : 0;
+        sInt[2] = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -203,8 +203,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const bool go = !__syncthreads_or(!good);
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(sInt[0]);
+    // (all CTAs see the same borders; a wait that expires is a second away)
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.status, go ? kDevOk : kDevParam);
     if (!go) {
-        if (threadIdx.x == 0) atomicExch(a.status, kDevParam);
     } else if (warp < 4) {
         reg_dealloc<kRegsFew>();
         if (warp == 0) {
@@ -256,7 +257,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     x = __shfl_sync(0xffffffffu, x, 0);
                     const int64_t now = x;
                     if (now < a.units) {
-                        if (lane == 0) x = take_unit(a);  // the next one, under this one's loads
+                        // the next one, under this one's loads
+                        if (lane == 0) x = a.units > gridDim.x ? take_unit(a) : a.units;
                         const int64_t ux = now / a.splits;
                         SeqTile st;
                         u.split = static_cast<int>(now % a.splits);
@@ -767,8 +769,7 @@ static cudaError_t launch_packed_fwd(const nabla::packed::Args &a, cudaStream_t 
         !nabla_make_tmap_view(&mv, keys ? a.v : a.q, keys ? a.total_k : 1, keys ? a.heads_kv : 1, D, 128, 1))
         return cudaErrorInvalidValue;
     constexpr uint32_t kSmem = FwdLayout<D>::kSmem;
-    cudaError_t err = cudaFuncSetAttribute(fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(kSmem));
+    cudaError_t err = nabla_allow_smem<fwd_kernel<D>>(kSmem);
     if (err != cudaSuccess) return err;
     const unsigned grid = static_cast<unsigned>(a.units < kSms ? a.units : kSms);
     fwd_kernel<D><<<grid, kFwdThreads, kSmem, stream>>>(mq, mk, mv, a);

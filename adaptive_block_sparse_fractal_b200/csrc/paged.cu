@@ -23,6 +23,7 @@
 // the ring and the softmax.  Scores, statistics and sums are float32; P
 // is rounded to bf16 for its MMA, its sum is taken in front of the rounding.
 #include "common.cuh"
+#include "launch.cuh"
 #include "paged.cuh"
 
 namespace nabla {
@@ -179,15 +180,6 @@ __device__ __forceinline__ int sharers(int64_t W, int ctas) { return W < ctas ? 
 // The share of CTA c of n: [W c / n, W (c + 1) / n), never empty
 __device__ __forceinline__ int64_t share(int64_t W, int c, int n) { return W * c / n; }
 
-// Programmatic dependent launch: the join starts beside the attention, up to
-// its wait, which returns when the attention has finished.
-__device__ __forceinline__ void allow_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_prerequisites() {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const __grid_constant__ PagedArgs a) {
     constexpr int kChunks = D / 8;  // 16-byte chunks a row
@@ -200,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const __grid_constan
     if (threadIdx.x == 0) any_bad = 0;
     bool bad = false;
 
-    allow_dependents();
+    allow_dependents();  // the join starts beside this launch, up to its wait
     // this CTA's run of units
     const int first_len = threadIdx.x < a.c.seqs ? clean_len(a, threadIdx.x, &bad) : 0;
     int64_t tiles = 0;
@@ -606,22 +598,12 @@ cudaError_t nabla_launch_append(const nabla::AppendArgs &a, cudaStream_t stream)
 template <int D>
 static cudaError_t launch_paged(const nabla::PagedArgs &a, cudaStream_t stream) {
     using namespace nabla::paged;
-    cudaError_t err = cudaFuncSetAttribute(paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(smem_bytes<D>()));
+    cudaError_t err = nabla_allow_smem<paged_kernel<D>>(smem_bytes<D>());
     if (err != cudaSuccess) return err;
     paged_kernel<D><<<a.ctas, kThreads, smem_bytes<D>(), stream>>>(a);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.c.seqs * a.heads));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D>, a);
+    return nabla_launch_early(join_kernel<D>, static_cast<unsigned>(a.c.seqs * a.heads), kThreads, 0, stream, a);
 }
 
 cudaError_t nabla_launch_paged(const nabla::PagedArgs &a, cudaStream_t stream) {

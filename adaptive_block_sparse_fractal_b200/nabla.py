@@ -6,6 +6,7 @@ fallback: if the library is missing or a call fails, this module raises.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -335,23 +336,24 @@ def _device(t, name):
     return dev
 
 
+# The structures of a call travel as packed bytes (half the cost of filling
+# ctypes structures): nabla_view, nabla_packed, and nabla_cache behind its views.
+_VIEW = struct.Struct("@Pqqq").pack
+_PACKED = struct.Struct("@iiiiqqif").pack
+_CACHE = struct.Struct("@Piiiiii").pack
+
+
 def _view(t, name, dev, dims, dtype, shape=None):
-    """(data, batch, head, token) of a tensor of rows on device dev.  Its last
-    dimension is contiguous; in front of it stand the tokens and heads ([tokens,
-    heads, D], dims = 3) or pages, rows and heads (dims = 4)."""
+    """nabla_view of a tensor of rows on device dev.  Its last dimension is
+    contiguous; in front of it stand the tokens and heads ([tokens, heads, D],
+    dims = 3) or pages, rows and heads (dims = 4)."""
     s = t.stride()
     if t.dtype != dtype or t.get_device() != dev or len(s) != dims or s[-1] != 1:
         raise ValueError("%s must be a %s tensor of %d dimensions on cuda:%d with a contiguous last "
                          "dimension" % (name, dtype, dims, dev))
     if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    return (t.data_ptr(), 0, s[1], s[0]) if dims == 3 else (t.data_ptr(), s[0], s[2], s[1])
-
-
-def _views(*views):
-    """References to consecutive nabla_view structures."""
-    a = (ctypes.c_int64 * (4 * len(views)))(*[x for v in views for x in v])
-    return [ctypes.byref(a, 32 * i) for i in range(len(views))]
+    return _VIEW(t.data_ptr(), 0, s[1], s[0]) if dims == 3 else _VIEW(t.data_ptr(), s[0], s[2], s[1])
 
 
 def _int32(t, name, dev, shape=None):
@@ -415,8 +417,7 @@ def rope(params, q, k=None, grid=None, pos=None, flat_in=False, flat_out=False, 
     T, H, W = grid
     if T * H * W != N:
         raise ValueError("grid %s does not hold %d tokens" % (tuple(grid), N))
-    values, heads = [[], []], (ctypes.c_int * 2)()
-    results = []
+    views, heads, results = [b"", b""], [0, 0], []
     for i, (x, y) in enumerate(((q, q_out), (k, k_out))):
         if x is None:
             break
@@ -433,7 +434,7 @@ def rope(params, q, k=None, grid=None, pos=None, flat_in=False, flat_out=False, 
             if t.dtype != dtype or t.get_device() != dev or (s[-1] != 1 and D > 1):
                 raise ValueError("q, k and the outputs must be %s tensors on cuda:%d with contiguous rows"
                                  % (dtype, dev))
-            values[side] += (t.data_ptr(), s[0] if dims == 4 else 0, s[-3], s[-2])
+            views[side] += _VIEW(t.data_ptr(), s[0] if dims == 4 else 0, s[-3], s[-2])
     pos_ptr, pos_batch, axes = None, 0, 0
     if pos is not None:
         axes = pos.shape[-1]
@@ -442,10 +443,8 @@ def rope(params, q, k=None, grid=None, pos=None, flat_in=False, flat_out=False, 
     p = RopeParams.from_buffer_copy(params)
     p.dtype, p.D = DTYPES[dtype], D
     p.flags |= (ROPE_FLAT_IN if flat_in else 0) | (ROPE_FLAT_OUT if flat_out else 0)
-    n = len(results)
-    _call(lib().nabla_rope, "nabla_rope", dev, ctypes.byref(p), B, T, H, W, P, n, heads,
-          (ctypes.c_int64 * (4 * n))(*values[0]), (ctypes.c_int64 * (4 * n))(*values[1]), pos_ptr,
-          pos_batch, axes)
+    _call(lib().nabla_rope, "nabla_rope", dev, ctypes.byref(p), B, T, H, W, P, len(results),
+          struct.pack("@ii", *heads), views[0], views[1], pos_ptr, pos_batch, axes)
     return results[0] if k is None else tuple(results)
 
 
@@ -454,16 +453,16 @@ def _packed_of(q, k, cu_q, causal, scale):
     D = shape[-1]
     if k.shape[-1] != D or len(shape) != 3:
         raise ValueError("q must be [total_q, heads, D] and k [total_k, heads_kv, D]")
-    return Packed(cu_q.shape[0] - 1, shape[1], k.shape[1], D, shape[0], k.shape[0],
-                  1 if causal else 0, D ** -0.5 if scale is None else scale)
+    return _PACKED(cu_q.shape[0] - 1, shape[1], k.shape[1], D, shape[0], k.shape[0],
+                   1 if causal else 0, D ** -0.5 if scale is None else scale)
 
 
 def packed_workspace(q, k, seqs, back=False):
     """Workspace of the packed calls for q [total_q, heads, D], k [total_k,
     heads_kv, D] and `seqs` sequences; back=True serves both directions.  It
     serves one call at a time."""
-    s = Packed(int(seqs), q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], 0, 1.0)
-    n = int(lib().nabla_packed_workspace_size(ctypes.byref(s), PACKED_BWD if back else PACKED_FWD))
+    s = _PACKED(int(seqs), q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], 0, 1.0)
+    n = int(lib().nabla_packed_workspace_size(s, PACKED_BWD if back else PACKED_FWD))
     if n == 0:
         raise NablaError(ERR_SHAPE, "nabla_packed_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=q.device)
@@ -479,17 +478,16 @@ def attn_packed_fwd(q, k, v, cu_q, cu_k, causal=False, scale=None, o=None, lse=N
     dev = _device(q, "q")
     bf = torch.bfloat16
     shape = _packed_of(q, k, cu_q, causal, scale)
-    views = [_view(q, "q", dev, 3, bf), _view(k, "k", dev, 3, bf), _view(v, "v", dev, 3, bf, k.shape)]
     if o is None:
         o = torch.empty_like(q)
-    views.append(_view(o, "o", dev, 3, bf, q.shape))
+    qs = q.shape
     if lse is None and want_lse:
-        lse = q.new_empty((q.shape[1], q.shape[0]), dtype=torch.float32)
-    lse_ptr = None if lse is None else _lse(lse, dev, (q.shape[1], q.shape[0]))
-    ws, ws_bytes = _work(packed_workspace(q, k, shape.seqs) if ws is None else ws, dev)
-    vq, vk, vv, vo = _views(*views)
-    _call(lib().nabla_attn_packed_fwd, "nabla_attn_packed_fwd", dev, ctypes.byref(shape), vq, vk, vv,
-          _int32(cu_q, "cu_q", dev), _int32(cu_k, "cu_k", dev, cu_q.shape), vo, lse_ptr, ws, ws_bytes)
+        lse = q.new_empty((qs[1], qs[0]), dtype=torch.float32)
+    lse_ptr = None if lse is None else _lse(lse, dev, (qs[1], qs[0]))
+    ws, ws_bytes = _work(packed_workspace(q, k, cu_q.shape[0] - 1) if ws is None else ws, dev)
+    _call(lib().nabla_attn_packed_fwd, "nabla_attn_packed_fwd", dev, shape, _view(q, "q", dev, 3, bf),
+          _view(k, "k", dev, 3, bf), _view(v, "v", dev, 3, bf, k.shape), _int32(cu_q, "cu_q", dev),
+          _int32(cu_k, "cu_k", dev, cu_q.shape), _view(o, "o", dev, 3, bf, qs), lse_ptr, ws, ws_bytes)
     return o, lse
 
 
@@ -503,25 +501,25 @@ def attn_packed_bwd(q, k, v, o, dout, lse, cu_q, cu_k, causal=False, scale=None,
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     qs, ks = q.shape, k.shape
-    vq, vk, vv, vo, vg, wq, wk, wv = _views(
-        _view(q, "q", dev, 3, bf), _view(k, "k", dev, 3, bf), _view(v, "v", dev, 3, bf, ks),
-        _view(o, "o", dev, 3, bf, qs), _view(dout, "dout", dev, 3, bf, qs),
-        _view(dq, "dq", dev, 3, bf, qs), _view(dk, "dk", dev, 3, bf, ks), _view(dv, "dv", dev, 3, bf, ks))
     lse_ptr = _lse(lse, dev, (qs[1], qs[0]))
-    ws, ws_bytes = _work(packed_workspace(q, k, shape.seqs, back=True) if ws is None else ws, dev)
-    _call(lib().nabla_attn_packed_bwd, "nabla_attn_packed_bwd", dev, ctypes.byref(shape), vq, vk, vv, vo,
-          vg, lse_ptr, _int32(cu_q, "cu_q", dev), _int32(cu_k, "cu_k", dev, cu_q.shape), wq, wk, wv, ws,
-          ws_bytes)
+    ws, ws_bytes = _work(packed_workspace(q, k, cu_q.shape[0] - 1, back=True) if ws is None else ws, dev)
+    _call(lib().nabla_attn_packed_bwd, "nabla_attn_packed_bwd", dev, shape, _view(q, "q", dev, 3, bf),
+          _view(k, "k", dev, 3, bf), _view(v, "v", dev, 3, bf, ks), _view(o, "o", dev, 3, bf, qs),
+          _view(dout, "dout", dev, 3, bf, qs), lse_ptr, _int32(cu_q, "cu_q", dev),
+          _int32(cu_k, "cu_k", dev, cu_q.shape), _view(dq, "dq", dev, 3, bf, qs),
+          _view(dk, "dk", dev, 3, bf, ks), _view(dv, "dv", dev, 3, bf, ks), ws, ws_bytes)
     return dq, dk, dv
 
 
 def _cache_of(k_cache, v_cache, table, seqs, dev):
-    shape = k_cache.shape
-    k = _view(k_cache, "k_cache", dev, 4, torch.bfloat16)
-    v = _view(v_cache, "v_cache", dev, 4, torch.bfloat16, shape)
+    """nabla_cache, heads_kv and D."""
+    pages, page, heads_kv, D = shape = k_cache.shape
     width = 1 if table is None else table.shape[-1]
-    ptr = None if table is None else _int32(table, "table", dev, (seqs, width))
-    return Cache(View(*k), View(*v), ptr, shape[0], shape[1], shape[2], shape[3], seqs, width)
+    ptr = 0 if table is None else _int32(table, "table", dev, (seqs, width))
+    c = (_view(k_cache, "k_cache", dev, 4, torch.bfloat16)
+         + _view(v_cache, "v_cache", dev, 4, torch.bfloat16, shape)
+         + _CACHE(ptr, pages, page, heads_kv, D, seqs, width))
+    return c, heads_kv, D
 
 
 def cache_workspace(device):
@@ -539,19 +537,19 @@ def cache_append(k, v, k_cache, v_cache, table, starts, cu=None, ws=None):
     seqs = starts.numel()
     starts_ptr = _int32(starts, "starts", dev, (seqs,))
     cu_ptr = None if cu is None else _int32(cu, "cu", dev, (seqs + 1,))
-    c = _cache_of(k_cache, v_cache, table, seqs, dev)
-    if tuple(k.shape[1:]) != (c.heads_kv, c.D):
-        raise ValueError("k must be [total, %d, %d]" % (c.heads_kv, c.D))
-    vk, vv = _views(_view(k, "k", dev, 3, torch.bfloat16), _view(v, "v", dev, 3, torch.bfloat16, k.shape))
+    c, heads_kv, D = _cache_of(k_cache, v_cache, table, seqs, dev)
+    shape = k.shape
+    if shape[1:] != (heads_kv, D):
+        raise ValueError("k must be [total, %d, %d]" % (heads_kv, D))
     ws, ws_bytes = (None, 0) if ws is None else _work(ws, dev)
-    _call(lib().nabla_cache_append, "nabla_cache_append", dev, ctypes.byref(c), vk, vv, k.shape[0],
-          starts_ptr, cu_ptr, ws, ws_bytes)
+    _call(lib().nabla_cache_append, "nabla_cache_append", dev, c, _view(k, "k", dev, 3, torch.bfloat16),
+          _view(v, "v", dev, 3, torch.bfloat16, shape), shape[0], starts_ptr, cu_ptr, ws, ws_bytes)
 
 
 def paged_workspace(q, k_cache):
     """Workspace of attn_paged; it serves one call at a time."""
-    c = _cache_of(k_cache, k_cache, None, 0, _device(k_cache, "k_cache"))
-    n = int(lib().nabla_paged_workspace_size(ctypes.byref(c), q.shape[1]))
+    c, _, _ = _cache_of(k_cache, k_cache, None, 0, _device(k_cache, "k_cache"))
+    n = int(lib().nabla_paged_workspace_size(c, q.shape[1]))
     if n == 0:
         raise NablaError(ERR_SHAPE, "nabla_paged_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=q.device)
@@ -566,19 +564,17 @@ def attn_paged(q, k_cache, v_cache, table, lens, scale=None, o=None, lse=None, w
     shape = q.shape
     view = _view(q, "q", dev, 3, bf)
     seqs, heads, D = shape
-    c = _cache_of(k_cache, v_cache, table, seqs, dev)
-    if c.D != D:
+    c, _, cache_D = _cache_of(k_cache, v_cache, table, seqs, dev)
+    if cache_D != D:
         raise ValueError("q and the cache must have the same D")
     if o is None:
         o = torch.empty_like(q)
     if lse is None and want_lse:
         lse = q.new_empty((seqs, heads), dtype=torch.float32)
     lse_ptr = None if lse is None else _lse(lse, dev, (seqs, heads))
-    vq, vo = _views(view, _view(o, "o", dev, 3, bf, shape))
     ws, ws_bytes = _work(paged_workspace(q, k_cache) if ws is None else ws, dev)
-    _call(lib().nabla_attn_paged, "nabla_attn_paged", dev, ctypes.byref(c), heads,
-          D ** -0.5 if scale is None else scale, vq, _int32(lens, "lens", dev, (seqs,)), vo, lse_ptr, ws,
-          ws_bytes)
+    _call(lib().nabla_attn_paged, "nabla_attn_paged", dev, c, heads, D ** -0.5 if scale is None else scale,
+          view, _int32(lens, "lens", dev, (seqs,)), _view(o, "o", dev, 3, bf, shape), lse_ptr, ws, ws_bytes)
     return o, lse
 
 
