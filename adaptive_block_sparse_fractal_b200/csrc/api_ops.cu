@@ -272,7 +272,7 @@ int nabla_rope(const nabla_rope_params *p, int B, int T, int H, int W, int P, in
     if (flat && (P < 1 || H % P != 0 || W % P != 0)) return NABLA_ERR_SHAPE;
     if (pos != nullptr && (pos_axes < 1 || pos_axes > 3 || pos_batch < 0)) return NABLA_ERR_PARAM;
     for (int i = 0; i < count; ++i)
-        if (heads[i] < 0 || heads[i] > (1 << 20)) return NABLA_ERR_SHAPE;
+        if (heads[i] < 0 || heads[i] > 32767) return NABLA_ERR_SHAPE;
     if (B == 0 || T == 0 || H == 0 || W == 0) return NABLA_OK;  // empty
     const int64_t N = static_cast<int64_t>(T) * H <= INT32_MAX / W ? static_cast<int64_t>(T) * H * W : -1;
     if (N < 0 || N > INT32_MAX - 256 || B > 65535) return NABLA_ERR_SHAPE;

@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
     constexpr int U = V * sizeof(T) == 16 && LAYOUT == 0 ? 8 : 4;  // heads in flight
     const int tok = blockIdx.x * blockDim.y + threadIdx.y;
     if (tok >= a.N) return;
-    const int b = blockIdx.y / a.head_splits;
-    const int h0 = (blockIdx.y % a.head_splits) * a.heads_per_cta;
+    const int b = blockIdx.z;
+    const int h0 = blockIdx.y * a.heads_per_cta;
     const int c = threadIdx.x;
     const int R = a.pairs;
 
@@ -185,9 +185,8 @@ static cudaError_t launch_rope(RopeArgs &a, cudaStream_t stream) {
     if (splits < (heads + 15) / 16) splits = (heads + 15) / 16;
     if (splits > heads) splits = heads;
     a.heads_per_cta = static_cast<int>((heads + splits - 1) / splits);
-    a.head_splits = (heads + a.heads_per_cta - 1) / a.heads_per_cta;
-    if (static_cast<int64_t>(a.B) * a.head_splits > 65535) return cudaErrorInvalidConfiguration;
-    rope_kernel<T, LAYOUT, V><<<dim3(static_cast<unsigned>(token_blocks), a.B * a.head_splits),
+    const int head_blocks = (heads + a.heads_per_cta - 1) / a.heads_per_cta;
+    rope_kernel<T, LAYOUT, V><<<dim3(static_cast<unsigned>(token_blocks), head_blocks, a.B),
                                 dim3(chunks, rows), 0, stream>>>(a);
     return cudaGetLastError();
 }

@@ -17,7 +17,7 @@ struct RopeTensor {
 struct RopeArgs {
     RopeTensor t[2];
     int count, B, N, T, H, W, P, D, pairs;
-    int flat_in, flat_out, heads_per_cta, head_splits;
+    int flat_in, flat_out, heads_per_cta;
     const int32_t *pos;  // [B or 1, N, pos_axes] or null: grid coordinates
     int64_t pos_batch;
     int pos_axes;

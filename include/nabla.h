@@ -335,7 +335,8 @@ typedef struct {
  * nabla_flatten (H and W multiples of P), so that rotation and flattening are
  * one pass; the gradient of a flattening call is the call with _INVERSE and
  * _IN / _OUT exchanged.
- * D even, 2 <= D <= 256.  Views whose pointers and distances are multiples of
+ * D even, 2 <= D <= 256, at most 32767 heads a tensor and 65535 batch entries.
+ * Views whose pointers and distances are multiples of
  * 16 bytes (and, in the HALVES layout, R a multiple of the elements in 16 bytes)
  * take 16-byte accesses; any other view is accepted as long as its pointers are
  * aligned to its elements.  An output may be its own input (same view, same
@@ -356,7 +357,11 @@ int nabla_rope(const nabla_rope_params *params, int B, int T, int H, int W, int 
  * written.  D in {64, 128}, at most 128 query heads a key head; pointers and
  * distances multiples of 16 bytes.
  * Borders that do not ascend, or that leave [0, total], make the call write
- * NABLA_ERR_PARAM to the workspace status and leave the outputs unwritten. */
+ * NABLA_ERR_PARAM to the workspace status and leave the outputs unwritten.
+ * NaN and infinities in rows of other sequences, or of none, never reach a
+ * sequence.  Inside one, a NaN or infinity of a row of v (backward: of q or dout)
+ * can also reach the rows of the same tile of up to 128 that mask it (causal).
+ * A workspace serves one call at a time. */
 typedef struct {
     int seqs, heads, heads_kv, D;
     int64_t total_q, total_k;

@@ -4,9 +4,9 @@ strides and far positions.
 Tolerance.  An output is a c - b s rounded once to its type.  With |c|, |s| <= 1
 and a, b the inputs, the float32 steps add at most 4 roundings of 2^-24 of
 (|a| + |b|), and the float32 sine and cosine of an exactly reduced angle are off
-by at most 2^-22 (sincospif is good to 2 units of 2^-24 and its argument, below
-1/4, is rounded at 2^-26, times pi).  So: half a step of the type relative to
-the value, plus 2^-21 (|a| + |b|)."""
+by at most 2^-22 (the series leave out less than 2^-25, their argument, below
+pi/4, is rounded at 2^-25, and a few roundings of 2^-25 follow).  So: half a step
+of the type relative to the value, plus 2^-21 (|a| + |b|)."""
 import pytest
 import torch
 
