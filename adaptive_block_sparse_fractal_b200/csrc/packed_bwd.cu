@@ -37,10 +37,103 @@ constexpr int kPreThreads = 256;
 // ---------------------------------------------------------------------------
 // delta and lse, padded: one CTA per 64 rows of a sequence and `per` heads
 // ---------------------------------------------------------------------------
+// delta = dout . o takes o as it was rounded to bf16.  With many keys that is
+// small against the rounding of dS; with few, dP - delta cancels and the rounding
+// of o stays: over sequences of 3 rows the gradients were off by 0.5%, of 2 rows
+// by 3%.  Tiles whose rows keep at most this many keys take o again in float32
+// (P as two bf16 terms, 2^-17), which brings them to the 0.23% of long ones.
+constexpr int kFewKeys = 32;
+
+// dout . o of 64 rows of head h over kmax <= kFewKeys keys, each half of the
+// features by four warps of 16 rows (m16n8k16, operands straight from global
+// memory: few tiles take this path, or few keys are there to read).
 template <int D>
-__global__ void __launch_bounds__(kPreThreads) pre_kernel(const __grid_constant__ Args a, int per) {
+__device__ __forceinline__ void exact_delta(const Args &a, const SeqTile &st, int h, int kmax, float (*part)[64]) {
+    constexpr int kN = D / 16;  // 8-feature tiles of a half
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rg = warp & 3, half = warp >> 2;
+    const int hk = h / a.group, off = st.Lk - st.Lq;
+    const int col = 2 * (lane & 3), sub = lane >> 2;
+    int row[2];
+    const __nv_bfloat16 *q[2], *g[2];
+    float nl[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        row[e] = st.tile * 64 + rg * 16 + sub + 8 * e;
+        const int64_t tok = st.q0 + min(row[e], st.Lq - 1);
+        q[e] = a.q.row(tok, h) + col;
+        g[e] = a.dout.row(tok, h) + half * (D / 2) + col;
+        nl[e] = -(a.lse[h * a.total_q + tok] * 1.4426950408889634f);
+    }
+    float acc[kN][4] = {};
+    for (int kb = 0; kb < kmax; kb += 16) {
+        float s[2][4] = {};
+#pragma unroll 4
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t qa[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                qa[e] = __ldg(reinterpret_cast<const uint32_t *>(q[e & 1] + 16 * kk + 8 * (e >> 1)));
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const __nv_bfloat16 *k = a.k.row(st.k0 + min(kb + 8 * n + sub, st.Lk - 1), hk) + 16 * kk + col;
+                mma_bf16(s[n], qa, __ldg(reinterpret_cast<const uint32_t *>(k)),
+                         __ldg(reinterpret_cast<const uint32_t *>(k + 8)));
+            }
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {  // operand register: row x & 1, keys 8 (x >> 1) + col, + 1
+            float p[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int key = kb + 8 * (x >> 1) + col + e;
+                const bool keep = key < st.Lk && (!a.causal || key <= row[x & 1] + off);
+                p[e] = keep ? fast_exp2(fmaf(s[x >> 1][2 * (x & 1) + e], a.c, nl[x & 1])) : 0.f;
+            }
+            hi[x] = pack_bf16(p[0], p[1]);
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&hi[x]));
+            lo[x] = pack_bf16(p[0] - f.x, p[1] - f.y);
+        }
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            uint32_t b[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t pair = 0;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int key = kb + 8 * x + col + e;
+                    if (key < st.Lk)
+                        pair |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(
+                                    a.v.row(st.k0 + key, hk) + half * (D / 2) + 8 * n + sub))) << (16 * e);
+                }
+                b[x] = pair;
+            }
+            mma_bf16(acc[n], hi, b[0], b[1]);
+            mma_bf16(acc[n], lo, b[0], b[1]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        float d = 0.f;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(g[e] + 8 * n));
+            d = fmaf(acc[n][2 * e], f.x, d);
+            d = fmaf(acc[n][2 * e + 1], f.y, d);
+        }
+        d += __shfl_xor_sync(0xffffffffu, d, 1);
+        d += __shfl_xor_sync(0xffffffffu, d, 2);
+        if ((lane & 3) == 0) part[half][rg * 16 + sub + 8 * e] = d;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPreThreads, 6) pre_kernel(const __grid_constant__ Args a, int per) {
     __shared__ SeqTile st;
     __shared__ int64_t sums[kPreThreads / 32];
+    __shared__ float part[2][64];
     allow_dependents();
     if (!find_seq<kPreThreads>(a, blockIdx.x, [](int Lq, int) { return (Lq + 63) >> 6; }, &st, sums))
         return;
@@ -48,8 +141,22 @@ __global__ void __launch_bounds__(kPreThreads) pre_kernel(const __grid_constant_
     constexpr int kStep = kPreThreads / TPR;
     const int sub = threadIdx.x % TPR;
     const int h1 = min(a.heads, static_cast<int>(blockIdx.y + 1) * per);
+    const int last = min(st.tile * 64 + 63, st.Lq - 1);
+    const int kmax = a.causal ? min(st.Lk, last + 1 + st.Lk - st.Lq) : st.Lk;  // keys of the tile's last row
     for (int h = blockIdx.y * per; h < h1; ++h) {
         const int64_t base = h * a.pad_rows + static_cast<int64_t>(st.pad + st.tile) * 64;
+        if (kmax > 0 && kmax <= kFewKeys) {
+            exact_delta<D>(a, st, h, kmax, part);
+            __syncthreads();
+            if (threadIdx.x < 64) {
+                const int r = threadIdx.x, i = st.tile * 64 + r;
+                const float L = i < st.Lq ? a.lse[h * a.total_q + st.q0 + i] : -INFINITY;
+                a.pad_d[base + r] = L == -INFINITY ? 0.f : -(part[0][r] + part[1][r]);
+                a.pad_l[base + r] = L == -INFINITY ? -INFINITY : -(L * 1.4426950408889634f);
+            }
+            __syncthreads();
+            continue;
+        }
 #pragma unroll
         for (int r = threadIdx.x / TPR; r < 64; r += kStep) {
             const int i = st.tile * 64 + r;

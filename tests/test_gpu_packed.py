@@ -303,3 +303,34 @@ def test_forward_scores_that_jump_far_above_the_first_tile(D, step):
         e = D * 2.0 ** -24 * (step + 20)
         seq_util.check(o, r["o"], r["o_tol"] * (1 + 4 * e / seq_util.H) + 4 * e * float(v.abs().max()), "o")
         seq_util.check(lse, r["lse"], 2.0 ** -20 * (1 + r["lse"].abs()) + 2.0 ** -18 + e, "lse")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens_q,lens_k,causal", [([2] * 40, [2] * 40, True), ([3, 2, 1, 4] * 8, [3, 2, 1, 4] * 8, True),
+                                                  ([70, 9], [2, 3], False), ([20, 31], [20, 31], True),
+                                                  ([200, 64], [32, 17], False)])
+def test_gradients_with_few_keys(lens_q, lens_k, causal, D):
+    """Few keys: dP - delta cancels, so delta must not carry the rounding of o.
+    The bound without that term: dS is rounded to bf16 once (h |dS|), and P (dP -
+    delta) has float32 errors e against its terms (E = 2^-14 covers the scores'
+    error, 2^-17 of P in delta and the sums)."""
+    q, k, v, dout, cq, ck, cu_q, cu_k = make(lens_q, lens_k, 4, 2, D, seed=21)
+    got = run_both(q, k, v, dout, cu_q, cu_k, causal)
+    sc, h = D ** -0.5, seq_util.H
+    for s in range(len(lens_q)):
+        a, b, c, e = cq[s], cq[s + 1], ck[s], ck[s + 1]
+        dk, dk_tol = 0, 0
+        for hd in range(4):
+            Q, K, V, G = q[a:b, hd].double(), k[c:e, hd // 2].double(), v[c:e, hd // 2].double(), dout[a:b, hd].double()
+            keep = seq_util.keep_mask(b - a, e - c, causal, "cuda")
+            x = seq_util.attention(Q, K, V, sc, keep, G)
+            p = ((Q @ K.T) * sc).masked_fill(~keep, -math.inf)
+            p = torch.softmax(p, 1)
+            dp = G @ V.T
+            ds = p * (dp - (G * x["o"]).sum(1, keepdim=True))
+            dds = h * ds.abs() + seq_util.E * p * (G.abs() @ V.abs().T + (G * x["o"]).abs().sum(1, keepdim=True))
+            seq_util.check(got[0][a:b, hd], x["dq"], (dds @ K.abs()) * sc + h * x["dq"].abs(), "dq")
+            dk, dk_tol = dk + x["dk"], dk_tol + (dds.T @ Q.abs()) * sc
+            if hd % 2:
+                seq_util.check(got[1][c:e, hd // 2], dk, dk_tol + h * dk.abs(), "dk")
+                dk, dk_tol = 0, 0
