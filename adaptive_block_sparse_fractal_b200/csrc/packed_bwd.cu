@@ -517,18 +517,17 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 // ---------------------------------------------------------------------------
 // Thread (g, r) of the two dS warpgroups handles row r and keys [32 g, +32) of
 // the tile and writes their bf16 dS over its own S columns [32 g, +16).  Two
-// warps issue: warp 1 the S and dP MMAs, warp 10 the dQ MMAs.  With three S
-// buffers the S MMAs of a tile wait only for the dQ MMAs of three tiles before,
-// and the one dP buffer is refilled once the dS warps hold the last tile's.
+// warps issue: warp 1 the S and dP MMAs, warp 10 the dQ MMAs.  S and dP have two
+// buffers each, so those of a tile run under the softmax of the one before.
 // Persistent: a CTA takes units (128 rows) from a counter; the dS warps fetch
 // the next unit's Q and dO rows into registers in front of the last one's
 // epilogue, and K and V tiles of the next unit run ahead in the ring.  With
 // one CTA a unit, 8 key tiles a unit took 11 us each, most of it start and end.
-// TMEM columns: S(t) [64 (t % 3), +64), dP [192, 256), dQ [256, 256 + D),
+// TMEM columns: S(t) [64 (t % 2), +64), dP(t) 128 further, dQ [256, 256 + D),
 // Q [384, 384 + D/2), dO [448, 448 + D/2).
 constexpr int kDqThreads = 352;
 constexpr int kDqGradWarp = 10;
-constexpr uint32_t kDqColDP = 192, kColDQ = 256, kColQ = 384, kColDO = 448;
+constexpr uint32_t kDqColDP = 128, kColDQ = 256, kColQ = 384, kColDO = 448;
 
 // One unit, as the loading warp hands it to the others.
 struct DqUnit {
@@ -545,7 +544,7 @@ struct DqLayout {
     static constexpr uint32_t kDqSlot = 2 * kBlockBytes;
     static constexpr uint32_t DQ_STAGE = kDqRing * kDqSlot;  // 2 KB per dS warp
     static constexpr uint32_t DQ_BAR = DQ_STAGE + 8 * 2048;
-    static constexpr int kBars = 2 * kDqRing + 3 + 3 + 1 + 1 + 3 + 1 + 1 + 1 + 4;
+    static constexpr int kBars = 2 * kDqRing + 2 + 2 + 1 + 1 + 2 + 1 + 1 + 4;
     static constexpr uint32_t DQ_UNIT = DQ_BAR + 8 * kBars;
     static constexpr uint32_t DQ_INT = (DQ_UNIT + 2 * sizeof(DqUnit) + 15) / 16 * 16;
     static constexpr uint32_t kSmem = DQ_INT + 16 + 1024;
@@ -567,9 +566,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     uint64_t *kv_full = bar, *kv_empty = bar + kDqRing, *s_full = bar + 2 * kDqRing;
     // per S buffer: s_full (S, dP complete), ds_full (the eight dS warps wrote
     // dS), s_free (the dQ MMAs have read it)
-    uint64_t *ds_full = s_full + 3, *q_ready = ds_full + 3, *done = q_ready + 1;
-    uint64_t *s_free = done + 1;
-    uint64_t *dp_free = s_free + 3, *sdp_done = dp_free + 1, *raw_full = sdp_done + 1;
+    uint64_t *ds_full = s_full + 2, *q_ready = ds_full + 2, *done = q_ready + 1;
+    uint64_t *s_free = done + 1, *sdp_done = s_free + 2, *raw_full = sdp_done + 1;
     uint64_t *u_full = raw_full + 1, *u_empty = u_full + 2;  // per unit slot; read by ten warps
     volatile DqUnit *units = reinterpret_cast<DqUnit *>(sm + L::DQ_UNIT);
     int *sInt = reinterpret_cast<int *>(sm + L::DQ_INT);  // [0] tmem base [2] abort
@@ -582,14 +580,13 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             mbar_init(&kv_full[r], 1);
             mbar_init(&kv_empty[r], 1);
         }
-        for (int b = 0; b < 3; ++b) {
+        for (int b = 0; b < 2; ++b) {
             mbar_init(&s_full[b], 1);
             mbar_init(&ds_full[b], 8);
             mbar_init(&s_free[b], 1);
         }
         mbar_init(q_ready, 8);
         mbar_init(done, 1);
-        mbar_init(dp_free, 8);
         mbar_init(sdp_done, 1);
         mbar_init(raw_full, 1);
         for (int b = 0; b < 2; ++b) {
@@ -696,8 +693,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         constexpr uint32_t kIdS = idesc_bf16(128, 64, 0, 0);    // Q . K^T, dO . V^T
         auto off = [](int kk) { return static_cast<uint32_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4); };
         int slot = 0, b = 0;
-        uint32_t kv_phase = 0, turn = 0, loaded = 0;  // turn: uses of the S buffers / 3; loaded: units with keys
-        uint32_t tiles = 0;
+        uint32_t kv_phase = 0, turn = 0, loaded = 0;  // turn: uses of the S buffers / 2; loaded: units with keys
         for (uint32_t n = 0; ok; ++n) {
             const int us = n & 1;
             ok = warp_wait(&u_full[us], (n >> 1) & 1u, abort_flag, a.status, a.limit);
@@ -708,9 +704,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             if (!valid) break;
             if (nt == 0) continue;
             ok = warp_wait(q_ready, loaded++ & 1u, abort_flag, a.status, a.limit);
-            for (int t = 0; ok && t < nt; ++t, ++tiles) {
+            for (int t = 0; ok && t < nt; ++t) {
                 ok = warp_wait(&kv_full[slot], kv_phase, abort_flag, a.status, a.limit);
-                // an S buffer is free once the dQ MMAs of its last tile have read its dS
+                // both buffers are free once the dQ MMAs of their last tile have read its dS
                 if (ok && turn > 0) ok = warp_wait(&s_free[b], (turn - 1) & 1u, abort_flag, a.status, a.limit);
                 if (!ok) break;
                 tc_fence_after();
@@ -718,22 +714,15 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 const uint32_t d = tmem + 64 * b;
                 // descriptors advance by (byte offset >> 4) in their low address field
                 const uint64_t dK = desc_sw128(b0, 16, 1024), dV = desc_sw128(b0 + kBlockBytes, 16, 1024);
-                // S first ...
+                const uint32_t e = tmem + kDqColDP + 64 * b;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; kk += 4)
                     mma_ts4_warp(d, d, d, d, tmem + kColQ + 8 * kk, tmem + kColQ + 8 * kk + 8,
                                  tmem + kColQ + 8 * kk + 16, tmem + kColQ + 8 * kk + 24, dK + off(kk),
                                  dK + off(kk + 1), dK + off(kk + 2), dK + off(kk + 3), kIdS, kk > 0, 1u);
-                // ... then dP into the single buffer, once the dS warps hold the last tile's
-                if (tiles > 0 && !warp_wait(dp_free, (tiles - 1) & 1u, abort_flag, a.status, a.limit)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < D / 16; kk += 4)
-                    mma_ts4_warp(tmem + kDqColDP, tmem + kDqColDP, tmem + kDqColDP, tmem + kDqColDP,
-                                 tmem + kColDO + 8 * kk, tmem + kColDO + 8 * kk + 8, tmem + kColDO + 8 * kk + 16,
+                    mma_ts4_warp(e, e, e, e, tmem + kColDO + 8 * kk, tmem + kColDO + 8 * kk + 8, tmem + kColDO + 8 * kk + 16,
                                  tmem + kColDO + 8 * kk + 24, dV + off(kk), dV + off(kk + 1), dV + off(kk + 2),
                                  dV + off(kk + 3), kIdS, kk > 0, 1u);
                 mma_commit_warp(&s_full[b]);
@@ -741,7 +730,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                     slot = 0;
                     kv_phase ^= 1u;
                 }
-                if (++b == 3) {
+                if (++b == 2) {
                     b = 0;
                     ++turn;
                 }
@@ -777,7 +766,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 mma_commit_warp(&kv_empty[slot]);
                 mma_commit_warp(&s_free[b]);
                 if (++slot == kDqRing) slot = 0;
-                if (++b == 3) {
+                if (++b == 2) {
                     b = 0;
                     phase ^= 1u;
                 }
@@ -863,12 +852,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 uint32_t gk[16];
                 float sv[32], dp[32];
                 tmem_ld32(scol, sv);
-                tmem_ld32(tmem + lane_base + kDqColDP + 32 * kg, dp);
+                tmem_ld32(scol + kDqColDP, dp);
                 tmem_wait_ld();
-                // dP is in registers: the buffer may take the next tile's
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(dp_free);
                 if (63 > left0) {  // masked tile: P = 0 and no NaN out of dP
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -889,7 +874,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ds_full[b]);
-                if (++b == 3) {
+                if (++b == 2) {
                     b = 0;
                     phase ^= 1u;
                 }
