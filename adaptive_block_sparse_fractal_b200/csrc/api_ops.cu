@@ -329,8 +329,12 @@ int nabla_rope(const nabla_rope_params *p, int B, int T, int H, int W, int P, in
     constexpr double kTwoPi = 6.283185307179586476925286766559;
     for (int ax = 0, at = 0; ax < 3; ++ax) {
         a.offset[ax] = p->pairs[ax] > 0 ? p->offset[ax] : 0.0;
+        // theta^(-i / n): a power for every eighth pair, products of up to 7 ratios
+        // between them (1e-15 relative; a pow a pair took 3 us of the call)
+        const double ratio = p->pairs[ax] > 0 ? std::pow(p->theta[ax], -1.0 / p->pairs[ax]) : 0.0;
+        double f = 1.0;
         for (int i = 0; i < p->pairs[ax]; ++i, ++at) {
-            const double f = std::pow(p->theta[ax], -static_cast<double>(i) / p->pairs[ax]);
+            f = i % 8 == 0 ? std::pow(p->theta[ax], -static_cast<double>(i) / p->pairs[ax]) : f * ratio;
             a.axis[at] = static_cast<int8_t>(ax);
             a.turn[at] = ((p->flags & NABLA_ROPE_INVERSE) ? -1.0 : 1.0) * p->scale[ax] * f / kTwoPi;
         }
@@ -377,7 +381,7 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
     a.lse = lse;
     a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kStatusBytes);
     a.splits = splits;
-    a.units = units * splits;
+    a.units = static_cast<uint32_t>(units * splits);
     return cuda_status(nabla_launch_packed_fwd(a, shape->D, s));
 }
 
@@ -431,7 +435,7 @@ int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const 
     a.dv = dev_view(dv);
     a.lse = const_cast<float *>(lse);
     a.pad_rows = q_tiles * 64;
-    a.units = row_tiles * shape->heads_kv;
+    a.units = static_cast<uint32_t>(row_tiles * shape->heads_kv);
     unsigned char *w = static_cast<unsigned char *>(workspace) + kStatusBytes;
     a.pad_l = reinterpret_cast<float *>(w);
     a.pad_d = reinterpret_cast<float *>(w + round256(sizeof(float) * a.pad_rows * shape->heads));

@@ -24,7 +24,8 @@ struct Args {
     int *status;       // workspace status word; behind it the unit counter
     float *pad_l, *pad_d;  // backward: [heads, pad_rows], -lse log2(e) and -dout.o
     float *part;       // split forward: partial rows, then their (m, l)
-    int64_t total_q, total_k, pad_rows, units;  // units: upper bound of the forward's
+    int64_t total_q, total_k, pad_rows;
+    uint32_t units;    // of a persistent launch, at most
     int seqs, heads, heads_kv, group, causal;
     int tile_tokens, splits;  // forward: tokens a row tile (128 / group), splits of the key range
     float c, scale;    // scale * log2(e), scale
@@ -112,8 +113,8 @@ __device__ __forceinline__ bool borders_ok(const Args &a) {
 // The next unit of a persistent launch, whose CTAs begin with the unit of their
 // own index (the counter starts at 0; the order in which CTAs take units does not
 // change what a unit computes).
-__device__ __forceinline__ int64_t take_unit(const Args &a) {
-    return static_cast<int64_t>(gridDim.x) + atomicAdd(reinterpret_cast<unsigned int *>(a.status) + 1, 1u);
+__device__ __forceinline__ uint32_t take_unit(const Args &a) {  // (units stay below 2^31)
+    return gridDim.x + atomicAdd(reinterpret_cast<unsigned int *>(a.status) + 1, 1u);
 }
 
 // One warp's walk over the sequences for units that only grow: 32 sequences at
@@ -121,12 +122,12 @@ __device__ __forceinline__ int64_t take_unit(const Args &a) {
 // ceil(Lq * mul / len) tiles.
 struct UnitScan {
     int base, q0, q1, k0, k1;
-    int64_t front, all;  // tiles in front of this lane's sequence and of the next 32
+    uint32_t front, all;     // tiles in front of this lane's sequence and of the next 32
     int pad_front, pad_all;  // the same of 64-row tiles of q
     __device__ __forceinline__ UnitScan()
         : base(-32), q0(0), q1(0), k0(0), k1(0), front(0), all(0), pad_front(0), pad_all(0) {}
     // sequence and tile of unit x; false behind the last
-    __device__ __forceinline__ bool find(const Args &a, int64_t x, int mul, int len, int lane, SeqTile *u) {
+    __device__ __forceinline__ bool find(const Args &a, uint32_t x, int mul, int len, int lane, SeqTile *u) {
         while (x >= all) {
             base += 32;
             if (base >= a.seqs) {
@@ -141,13 +142,13 @@ struct UnitScan {
                 k0 = a.cu_k[s];
                 k1 = a.cu_k[s + 1];
             }
-            const int64_t mine = ((q1 - q0) * mul + len - 1) / len;
+            const uint32_t mine = (static_cast<uint32_t>(q1 - q0) * mul + len - 1) / len;
             const int pads = (q1 - q0 + 63) >> 6;
-            int64_t incl = mine;
+            uint32_t incl = mine;
             int pincl = pads;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+                const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
                 const int p = __shfl_up_sync(0xffffffffu, pincl, o);
                 if (lane >= o) {
                     incl += t;

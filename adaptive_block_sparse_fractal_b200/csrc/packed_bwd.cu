@@ -614,18 +614,19 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             prefetch_tmap(&tv);
         }
         UnitScan scan;
-        int64_t x = blockIdx.x;
+        uint32_t x = blockIdx.x;
         uint32_t seq = 0, tails = 0;
         for (uint32_t n = 0; ok; ++n) {
             const int us = n & 1;
             DqUnit u = {};
             x = __shfl_sync(0xffffffffu, x, 0);
-            const int64_t now = x;
+            const uint32_t now = x;
             if (now < a.units) {
                 if (lane == 0) x = take_unit(a);  // the next one, under this one's loads
                 SeqTile st;
-                u.hk = static_cast<int>(now % a.heads_kv);
-                u.valid = scan.find(a, now / a.heads_kv, G, 128, lane, &st);
+                const uint32_t hkv = a.heads_kv;
+                u.hk = static_cast<int>(now % hkv);
+                u.valid = scan.find(a, now / hkv, G, 128, lane, &st);
                 if (u.valid) {
                     u.q0 = st.q0;
                     u.Lq = st.Lq;
