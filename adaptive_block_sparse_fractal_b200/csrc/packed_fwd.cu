@@ -73,9 +73,11 @@ constexpr int kRegsFew = 64, kRegsMany = 104;
 constexpr int kTileKeys = 128;
 constexpr float kFwdLn2 = 0.6931471805599453f;
 constexpr float kMaxSum = 1152921504606846976.f;  // 2^60: largest sum of P over a tile's half row
-// pairs of every 8 whose exponentials the FMA pipe takes (D = 128 dense: 1 of 8
-// 1,332 TFLOP/s, 2 1,381, 3 1,332)
-constexpr int kPolyOf8 = 2;
+// pairs of every 8 whose exponentials the FMA pipe takes.  D = 128, dense: 1 of 8
+// 1,332 TFLOP/s, 2 1,381, 3 1,332; D = 64, where the tensor core has half the
+// work and instruction issue is short: 0 739, 1 785, 2 760, 3 704.
+template <int D>
+constexpr int kPolyOf8 = D == 128 ? 2 : 1;
 
 // One unit, as the loading warp hands it to the others.
 struct Unit {
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         uint32_t pk[16];
                         tmem_ld32(scol + 32 * part, s);
                         tmem_wait_ld_of(s);
-                        softmax_part<kPolyOf8>(s, c2, nm2, ls2, pk);
+                        softmax_part<kPolyOf8<D>>(s, c2, nm2, ls2, pk);
                         tmem_st16(scol + 16 * part, pk);
                         hand_over(part);
                     }
