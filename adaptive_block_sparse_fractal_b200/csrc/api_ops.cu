@@ -28,6 +28,8 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? NABLA_OK : NABLA_ERR_CUDA; }
 cudaStream_t as_stream(nabla_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 int check_workspace(const void *ws, size_t bytes, size_t need) {
     if (ws == nullptr || bytes < need) return NABLA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return NABLA_ERR_ALIGN;
@@ -177,8 +179,7 @@ int check_packed(const nabla_packed *s, const int32_t *cu_q, const int32_t *cu_k
     if (!(s->scale > 0.f) || !std::isfinite(s->scale) || (s->causal != 0 && s->causal != 1))
         return NABLA_ERR_PARAM;
     if (cu_q == nullptr || cu_k == nullptr) return NABLA_ERR_NULL;
-    if (((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) & 3u) != 0)
-        return NABLA_ERR_ALIGN;
+    if (!aligned4(cu_q) || !aligned4(cu_k)) return NABLA_ERR_ALIGN;
     return check_workspace(ws, bytes, packed_ws(s, op));
 }
 
@@ -213,7 +214,7 @@ bool cache_shape_ok(const nabla_cache *c) {
 
 int check_cache(const nabla_cache *c, bool written, Box bx[2], nabla::CacheArgs *a) {
     if (c->k.data == nullptr || c->v.data == nullptr || c->table == nullptr) return NABLA_ERR_NULL;
-    if ((reinterpret_cast<uintptr_t>(c->table) & 3u) != 0) return NABLA_ERR_ALIGN;
+    if (!aligned4(c->table)) return NABLA_ERR_ALIGN;
     const nabla_view *v[2] = {&c->k, &c->v};
     for (int i = 0; i < 2; ++i) {
         if (!make_box(v[i], c->pages, c->heads_kv, c->page_size, c->D, 2, &bx[i]))
@@ -271,6 +272,7 @@ int nabla_rope(const nabla_rope_params *p, int B, int T, int H, int W, int P, in
     const bool flat = (p->flags & (NABLA_ROPE_FLAT_IN | NABLA_ROPE_FLAT_OUT)) != 0;
     if (flat && (P < 1 || H % P != 0 || W % P != 0)) return NABLA_ERR_SHAPE;
     if (pos != nullptr && (pos_axes < 1 || pos_axes > 3 || pos_batch < 0)) return NABLA_ERR_PARAM;
+    if (!aligned4(pos)) return NABLA_ERR_ALIGN;
     for (int i = 0; i < count; ++i)
         if (heads[i] < 0 || heads[i] > 32767) return NABLA_ERR_SHAPE;
     if (B == 0 || T == 0 || H == 0 || W == 0) return NABLA_OK;  // empty
@@ -361,6 +363,7 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
         (st = packed_view(v, shape->total_k, shape->heads_kv, shape->D, false, &bv)) != NABLA_OK ||
         (st = packed_view(o, shape->total_q, shape->heads, shape->D, true, &bo)) != NABLA_OK)
         return st;
+    if (!aligned4(lse)) return NABLA_ERR_ALIGN;
     if (shape->total_q > 0 && (!disjoint(bo, bq) || (shape->total_k > 0 &&
                                                      (!disjoint(bo, bk) || !disjoint(bo, bv)))))
         return NABLA_ERR_PARAM;
@@ -404,6 +407,7 @@ int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const 
     for (int i = 0; i < 3; ++i)
         if ((st = view(out[i], out_q[i], true, &bo[i])) != NABLA_OK) return st;
     if (shape->total_q > 0 && lse == nullptr) return NABLA_ERR_NULL;
+    if (!aligned4(lse)) return NABLA_ERR_ALIGN;
     // the three kernels read the inputs while the first outputs are written
     for (int i = 0; i < 3; ++i) {
         if ((out_q[i] ? shape->total_q : shape->total_k) == 0) continue;
@@ -460,8 +464,7 @@ int nabla_cache_append(const nabla_cache *cache, const nabla_view *k, const nabl
         const int st = check_cache(cache, true, pool, &a.c);
         if (st != NABLA_OK) return st;
         if (k->data == nullptr || v->data == nullptr || starts == nullptr) return NABLA_ERR_NULL;
-        if (((reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(cu)) & 3u) != 0)
-            return NABLA_ERR_ALIGN;
+        if (!aligned4(starts) || !aligned4(cu)) return NABLA_ERR_ALIGN;
         if (!make_box(k, 1, cache->heads_kv, total, cache->D, 2, &bk) ||
             !make_box(v, 1, cache->heads_kv, total, cache->D, 2, &bv))
             return NABLA_ERR_PARAM;
@@ -512,7 +515,7 @@ int nabla_attn_paged(const nabla_cache *cache, int heads, float scale, const nab
     Box pool[2], bq, bo;
     if ((st = check_cache(cache, false, pool, &a.c)) != NABLA_OK) return st;
     if (q->data == nullptr || o->data == nullptr || lens == nullptr) return NABLA_ERR_NULL;
-    if ((reinterpret_cast<uintptr_t>(lens) & 3u) != 0) return NABLA_ERR_ALIGN;
+    if (!aligned4(lens) || !aligned4(lse)) return NABLA_ERR_ALIGN;
     if (!make_box(q, 1, heads, cache->seqs, cache->D, 2, &bq) ||
         !make_box(o, 1, heads, cache->seqs, cache->D, 2, &bo))
         return NABLA_ERR_PARAM;

@@ -482,7 +482,7 @@ def attn_packed_fwd(q, k, v, cu_q, cu_k, causal=False, scale=None, o=None, lse=N
         o = torch.empty_like(q)
     qs = q.shape
     if lse is None and want_lse:
-        lse = q.new_empty((qs[1], qs[0]), dtype=torch.float32)
+        lse = torch.empty_strided((qs[1], qs[0]), (qs[0], 1), dtype=torch.float32, device=q.device)
     lse_ptr = None if lse is None else _lse(lse, dev, (qs[1], qs[0]))
     ws, ws_bytes = _work(packed_workspace(q, k, cu_q.shape[0] - 1) if ws is None else ws, dev)
     _call(lib().nabla_attn_packed_fwd, "nabla_attn_packed_fwd", dev, shape, _view(q, "q", dev, 3, bf),
@@ -570,7 +570,7 @@ def attn_paged(q, k_cache, v_cache, table, lens, scale=None, o=None, lse=None, w
     if o is None:
         o = torch.empty_like(q)
     if lse is None and want_lse:
-        lse = q.new_empty((seqs, heads), dtype=torch.float32)
+        lse = torch.empty_strided((seqs, heads), (heads, 1), dtype=torch.float32, device=q.device)
     lse_ptr = None if lse is None else _lse(lse, dev, (seqs, heads))
     ws, ws_bytes = _work(paged_workspace(q, k_cache) if ws is None else ws, dev)
     _call(lib().nabla_attn_paged, "nabla_attn_paged", dev, c, heads, D ** -0.5 if scale is None else scale,

@@ -55,6 +55,7 @@ def test_rope_rejects_on_host(L):
     assert rope(L, pos=pos, axes=0) == nabla.ERR_PARAM
     assert rope(L, pos=pos, axes=2) == nabla.ERR_PARAM           # three axes are turned
     assert rope(L, pos=pos, axes=3, pos_batch=-1) == nabla.ERR_PARAM
+    assert rope(L, pos=ctypes.c_void_p(BASE + 2), axes=3) == nabla.ERR_ALIGN
     n, D = 4 * 16 * 16, 128
     v = lambda addr, token=D, head=n * D: nabla.View(addr, 0, head, token)
     far = 1 << 30
@@ -204,6 +205,7 @@ def test_packed_backward_rejects_on_host(L):
         assert call(**{n: None}) == nabla.ERR_NULL
         assert call(**{n: view(BASE + 20 * far + 4, 1024)}) == nabla.ERR_ALIGN
     assert call(lse=None) == nabla.ERR_NULL
+    assert call(lse=BASE + 2) == nabla.ERR_ALIGN
     assert call(ws_bytes=256) == nabla.ERR_WORKSPACE
     assert call(dq=view(BASE + far, 1024)) == nabla.ERR_PARAM         # dq is q
     assert call(dk=view(BASE + 8 * far, 1024)) == nabla.ERR_PARAM     # dk is dv
