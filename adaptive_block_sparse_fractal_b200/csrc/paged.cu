@@ -471,17 +471,17 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const __grid_constan
 }
 
 // One CTA per (sequence, query head): adds the pieces of the CTAs that shared
-// it, in order, four warps taking every fourth piece; writes empty rows; the
+// it, in order, its NW warps taking every NW-th piece; writes empty rows; the
 // first CTA gathers the flags into the status word.
-template <int D>
-__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ PagedArgs a) {
-    constexpr int kPer = D / 32;
-    __shared__ int64_t sums[2 * kWarps];
-    __shared__ float so[kWarps][D], sw[kPagedCtas], part[2][kWarps];
+template <int D, int NW>
+__global__ void __launch_bounds__(32 * NW) join_kernel(const __grid_constant__ PagedArgs a) {
+    constexpr int kPer = D / 32, NT = 32 * NW;
+    __shared__ int64_t sums[2 * NW];
+    __shared__ float so[NW][D], sw[kPagedCtas], part[2][NW];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
     int64_t front, tiles;
-    tile_sums<kThreads>(a, s, sums, &front, &tiles);
+    tile_sums<NT>(a, s, sums, &front, &tiles);
     bool bad = false;
     const int nt = tiles_of(clean_len(a, s, &bad));
     const int per_seq = a.c.heads_kv * a.chunks;
@@ -497,15 +497,15 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     }
     wait_for_prerequisites();
     if (blockIdx.x == 0) {
-        for (int i = threadIdx.x; i < a.c.seqs; i += kThreads) clean_len(a, i, &bad);
-        for (int i = threadIdx.x; i < a.ctas; i += kThreads) bad |= a.flags[i] != 0;
+        for (int i = threadIdx.x; i < a.c.seqs; i += NT) clean_len(a, i, &bad);
+        for (int i = threadIdx.x; i < a.ctas; i += NT) bad |= a.flags[i] != 0;
         bad = __syncthreads_or(bad);
         if (threadIdx.x == 0) *a.status = bad ? kDevParam : kDevOk;
     }
     __nv_bfloat16 *dst = a.o + s * a.o_token + head * a.o_head;
     float *lse = a.lse == nullptr ? nullptr : a.lse + static_cast<int64_t>(s) * a.heads + head;
     if (nt == 0) {
-        for (int d = threadIdx.x; d < D; d += kThreads) dst[d] = __float2bfloat16_rn(0.f);
+        for (int d = threadIdx.x; d < D; d += NT) dst[d] = __float2bfloat16_rn(0.f);
         if (threadIdx.x == 0 && lse != nullptr) *lse = -INFINITY;
         return;
     }
@@ -514,10 +514,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     const float2 *ml = reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(2 * a.ctas) * kPagedHeads * D);
     // piece p: the first one began in its CTA (slot 1), the others in an earlier one (slot 0)
     auto slot_of = [&](int p) { return static_cast<int64_t>(2 * (c0 + p) + (p == 0 ? 1 : 0)) * kPagedHeads + r; };
-    float m[(kPagedCtas + kThreads - 1) / kThreads], l[(kPagedCtas + kThreads - 1) / kThreads], M = -INFINITY;
+    float m[(kPagedCtas + NT - 1) / NT], l[(kPagedCtas + NT - 1) / NT], M = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < (kPagedCtas + kThreads - 1) / kThreads; ++i) {
-        const int p = i * kThreads + threadIdx.x;
+    for (int i = 0; i < (kPagedCtas + NT - 1) / NT; ++i) {
+        const int p = i * NT + threadIdx.x;
         m[i] = -INFINITY;
         l[i] = 0.f;
         if (p < pieces) {
@@ -532,12 +532,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     if (lane == 0) part[0][warp] = M;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part[0][w]);
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, part[0][w]);
     const float R = M == -INFINITY ? 0.f : M;
     float total = 0.f;
 #pragma unroll
-    for (int i = 0; i < (kPagedCtas + kThreads - 1) / kThreads; ++i) {
-        const int p = i * kThreads + threadIdx.x;
+    for (int i = 0; i < (kPagedCtas + NT - 1) / NT; ++i) {
+        const int p = i * NT + threadIdx.x;
         const float w = fast_exp2(m[i] - R);
         if (p < pieces) sw[p] = w;
         total += w * l[i];
@@ -548,12 +548,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     __syncthreads();
     total = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += part[1][w];
+    for (int w = 0; w < NW; ++w) total += part[1][w];
     float o[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[e] = 0.f;
 #pragma unroll 8
-    for (int p = warp; p < pieces; p += kWarps) {
+    for (int p = warp; p < pieces; p += NW) {
         const float *src = a.part + slot_of(p) * D + lane * kPer;
         const float w = sw[p];
         if constexpr (kPer == 4) {
@@ -572,10 +572,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = o[e];
     __syncthreads();
     const float inv = total == 0.f ? 0.f : 1.f / total;
-    for (int d = threadIdx.x; d < D; d += kThreads) {
+    for (int d = threadIdx.x; d < D; d += NT) {
         float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) x += so[w][d];
+        for (int w = 0; w < NW; ++w) x += so[w][d];
         dst[d] = __float2bfloat16_rn(x * inv);
     }
     if (threadIdx.x == 0 && lse != nullptr)
@@ -603,7 +603,11 @@ static cudaError_t launch_paged(const nabla::PagedArgs &a, cudaStream_t stream) 
     paged_kernel<D><<<a.ctas, kThreads, smem_bytes<D>(), stream>>>(a);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    return nabla_launch_early(join_kernel<D>, static_cast<unsigned>(a.c.seqs * a.heads), kThreads, 0, stream, a);
+    // few rows to join may each have hundreds of pieces (one sequence of 100,000
+    // keys, 8 heads on one key head): 16 warps a row; many rows have few each
+    const unsigned rows = static_cast<unsigned>(a.c.seqs * a.heads);
+    return rows <= 148 ? nabla_launch_early(join_kernel<D, 16>, rows, 512, 0, stream, a)
+                       : nabla_launch_early(join_kernel<D, 4>, rows, 128, 0, stream, a);
 }
 
 cudaError_t nabla_launch_paged(const nabla::PagedArgs &a, cudaStream_t stream) {
