@@ -174,3 +174,70 @@ def test_two_streams_with_their_own_workspaces():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# ---------------------------------------------------------------------------
+# offsets beyond 2^31 elements
+# ---------------------------------------------------------------------------
+FAR = 2 ** 31
+
+
+def test_far_rows_of_packed_tensors():
+    """Sequences whose rows lie behind the first 2^31 elements of every tensor."""
+    heads, D = 40, 128
+    total = FAR // (heads * D) + 700
+    cu = [total - 650, total - 350, total - 349, total - 5]
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def make():
+        t = torch.empty(total, heads, D, dtype=BF, device="cuda")
+        t[total - 700:] = torch.randn(700, heads, D, generator=g, device="cuda").to(BF)
+        return t
+    q, k, v, dout = make(), make(), make(), make()
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    ws = nabla.packed_workspace(q, k, 3, back=True)
+    o, lse = nabla.attn_packed_fwd(q, k, v, cud, cud, causal=True, ws=ws)
+    assert nabla.status(ws) == nabla.OK
+    dq, dk, dv = nabla.attn_packed_bwd(q, k, v, o, dout, lse, cud, cud, causal=True, ws=ws)
+    assert nabla.status(ws) == nabla.OK
+    a = total - 700
+    near = [c - a for c in cu]
+    pick = lambda t: t[a:, 17:18].contiguous()
+    r = seq_util.packed(pick(q), pick(k), pick(v), near, near, True, dout=pick(dout))
+    for n, t in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv)):
+        seq_util.check(pick(t), r[n], r[n + "_tol"], n)
+    seq_util.check_lse(lse[17:18, a:], r["lse"])
+
+
+def test_far_pages_and_far_rope_rows():
+    page, heads_kv, D = 64, 4, 128
+    pages = FAR // (page * heads_kv * D) + 20
+    kc = torch.empty(pages, page, heads_kv, D, dtype=BF, device="cuda")
+    vc = torch.empty_like(kc)
+    table = torch.tensor([[pages - 1, pages - 3, 0], [pages - 2, pages - 7, pages - 5]], dtype=torch.int32,
+                         device="cuda")
+    lens = [130, 190]
+    cu = torch.tensor([0, 130, 320], dtype=torch.int32, device="cuda")
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(320, heads_kv, D, device="cuda").to(BF) for _ in range(2))
+    nabla.cache_append(k, v, kc, vc, table, zero, cu=cu)
+    q = torch.randn(2, 8, D, device="cuda").to(BF)
+    o, _ = nabla.attn_paged(q, kc, vc, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    for s, (a, b) in enumerate(((0, 130), (130, 320))):
+        for h in range(8):
+            x = seq_util.attention(q[s, h:h + 1].double(), k[a:b, h // 2].double(), v[a:b, h // 2].double(),
+                                   D ** -0.5, torch.ones(1, b - a, dtype=torch.bool, device="cuda"))
+            seq_util.check(o[s, h:h + 1], x["o"], x["o_tol"], "o")
+    del kc, vc
+    # rotation in place of rows behind 2^31 elements, tokens first
+    heads = 20
+    total = FAR // (heads * D) + 300
+    x = torch.empty(total, heads, D, dtype=BF, device="cuda")
+    tail = torch.randn(300, heads, D, device="cuda").to(BF)
+    x[total - 300:] = tail
+    prm = nabla.rope_params_of((64,))
+    pos = torch.arange(total, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    y = x.transpose(0, 1)
+    nabla.rope(prm, y, pos=pos, q_out=y)
+    want = nabla.rope(prm, tail.transpose(0, 1), pos=pos[total - 300:].contiguous())
+    assert torch.equal(x[total - 300:].transpose(0, 1), want)
