@@ -42,6 +42,8 @@ constexpr int kPreThreads = 256;
 // of o stays: over sequences of 3 rows the gradients were off by 0.5%, of 2 rows
 // by 3%.  Tiles whose rows keep at most this many keys take o again in float32
 // (P as two bf16 terms, 2^-17), which brings them to the 0.23% of long ones.
+// (Up to 128 keys would cost 290 us in a cross attention of 3,000 rows and 24 heads
+// to 77 keys, to go from 0.28% to 0.23%.)
 constexpr int kFewKeys = 32;
 
 // dout . o of 64 rows of head h over kmax <= kFewKeys keys, each half of the
