@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.group, tpt = a.tile_tokens;  // tokens a row tile
 
+    allow_dependents();  // combine_kernel, up to its wait
     if (threadIdx.x == 0) {
         for (int r = 0; r < kRing; ++r) {
             mbar_init(&kv_full[r], 1);
@@ -693,6 +694,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Args a) {
     const int splits = a.splits;
+    wait_for_prerequisites();
     if (*reinterpret_cast<volatile int *>(a.status) != 0) return;
     const int lane = threadIdx.x & 31;
     const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -780,8 +782,7 @@ static cudaError_t launch_packed_fwd(const nabla::packed::Args &a, cudaStream_t 
     err = cudaGetLastError();
     if (err != cudaSuccess || a.splits == 1) return err;
     const int64_t rows = a.total_q * a.heads;
-    combine_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return nabla_launch_early(combine_kernel<D>, static_cast<unsigned>((rows + 7) / 8), 256, 0, stream, a);
 }
 
 cudaError_t nabla_launch_packed_fwd(const nabla::packed::Args &a, int D, cudaStream_t stream) {
