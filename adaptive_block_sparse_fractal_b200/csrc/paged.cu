@@ -40,6 +40,38 @@ constexpr float kLn2 = 0.6931471805599453f;
 // ---------------------------------------------------------------------------
 constexpr int kAppendTokens = 8;  // most tokens a CTA takes
 
+// Element offsets of a token's rows in the pools, -1 for a token that is not
+// written; true when that is because its place is out of range.
+__device__ __forceinline__ bool find_place(const AppendArgs &a, int64_t tok, int64_t *pk, int64_t *pv) {
+    int s = -1;
+    int64_t i = 0;
+    *pk = *pv = -1;
+    if (a.cu == nullptr) {
+        s = static_cast<int>(tok);
+    } else if (tok >= a.cu[0] && tok < a.cu[a.c.seqs]) {
+        int lo = 0, hi = a.c.seqs;  // last s with cu[s] <= tok
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.cu[mid] <= tok)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        s = lo;
+        i = tok - a.cu[s];
+    }
+    if (s < 0) return false;  // of no sequence
+    const int64_t p = a.starts[s] + i;
+    const int64_t col = p / a.c.page_size;
+    int page = -1;
+    if (p >= 0 && i >= 0 && col < a.c.width) page = a.c.table[static_cast<int64_t>(s) * a.c.width + col];
+    if (page < 0 || page >= a.c.pages) return true;
+    const int64_t r = p - col * a.c.page_size;
+    *pk = page * a.c.k_page + r * a.c.k_token;
+    *pv = page * a.c.v_page + r * a.c.v_token;
+    return false;
+}
+
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendArgs a, int per_cta) {
     constexpr int U = 4;  // pieces a thread has in flight
     __shared__ int64_t place[2][kAppendTokens];
@@ -67,43 +99,24 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
         }
     };
     fetch(threadIdx.x);  // the first pieces travel while the places are looked up
-    if (threadIdx.x < tokens) {
-        const int64_t tok = t0 + threadIdx.x;
-        int64_t pk = -1, pv = -1;
-        int s = -1;
-        int64_t i = 0;
-        if (a.cu == nullptr) {
-            s = static_cast<int>(tok);
-        } else if (tok >= a.cu[0] && tok < a.cu[a.c.seqs]) {
-            int lo = 0, hi = a.c.seqs;  // last s with cu[s] <= tok
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (a.cu[mid] <= tok)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            s = lo;
-            i = tok - a.cu[s];
+    // (with status_by_kernel the first CTA looks at the other CTAs' tokens too)
+    const bool all = a.status_by_kernel && blockIdx.x == 0;
+    bool bad = false;
+    if (threadIdx.x < (all ? static_cast<int>(a.total) : tokens)) {
+        int64_t pk, pv;
+        bad = find_place(a, t0 + threadIdx.x, &pk, &pv);
+        if (threadIdx.x < tokens) {
+            place[0][threadIdx.x] = pk;
+            place[1][threadIdx.x] = pv;
         }
-        if (s >= 0) {
-            const int64_t p = a.starts[s] + i;
-            const int64_t col = p / a.c.page_size;
-            int page = -1;
-            if (p >= 0 && i >= 0 && col < a.c.width)
-                page = a.c.table[static_cast<int64_t>(s) * a.c.width + col];
-            if (page >= 0 && page < a.c.pages) {
-                const int64_t r = p - col * a.c.page_size;
-                pk = page * a.c.k_page + r * a.c.k_token;
-                pv = page * a.c.v_page + r * a.c.v_token;
-            } else if (a.status != nullptr) {
-                atomicExch(a.status, kDevParam);
-            }
-        }
-        place[0][threadIdx.x] = pk;
-        place[1][threadIdx.x] = pv;
     }
-    __syncthreads();
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0 && a.status != nullptr) {
+        if (all)
+            *a.status = bad ? kDevParam : kDevOk;
+        else if (bad && !a.status_by_kernel)
+            atomicExch(a.status, kDevParam);
+    }
     for (int base = threadIdx.x; base < n; base += U * 256) {
         if (base != threadIdx.x) fetch(base);
 #pragma unroll

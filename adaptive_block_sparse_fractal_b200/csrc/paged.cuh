@@ -25,6 +25,7 @@ struct AppendArgs {
     const int32_t *starts, *cu;
     int64_t total;
     int *status;
+    int status_by_kernel;  // the first CTA writes the status word (total <= 256)
 };
 
 struct PagedArgs {

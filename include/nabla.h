@@ -354,7 +354,7 @@ int nabla_rope(const nabla_rope_params *params, int B, int T, int H, int W, int 
  *   causal  row i of Lq keeps the keys j <= i + Lk - Lq of its sequence (the
  *           last rows of both coincide); otherwise it keeps all of them.
  * Rows of q and k that belong to no sequence are neither read into a result nor
- * written.  D in {64, 128}, at most 128 query heads a key head; pointers and
+ * written.  D in {64, 128}, at most 65535 heads, 128 of them a key head; pointers and
  * distances multiples of 16 bytes.
  * Borders that do not ascend, or that leave [0, total], make the call write
  * NABLA_ERR_PARAM to the workspace status and leave the outputs unwritten.
