@@ -341,6 +341,7 @@ def _device(t, name):
 _VIEW = struct.Struct("@Pqqq").pack
 _PACKED = struct.Struct("@iiiiqqif").pack
 _CACHE = struct.Struct("@Piiiiii").pack
+_HEADS = struct.Struct("@ii").pack
 
 
 def _view(t, name, dev, dims, dtype, shape=None):
@@ -403,49 +404,56 @@ def rope(params, q, k=None, grid=None, pos=None, flat_in=False, flat_out=False, 
     by `pos` (int32 [N, axes] or [B, N, axes], in grid order).  flat_in /
     flat_out: that side is in flattened token order (needs `grid`).  Outputs may
     be the inputs (same order on both sides).  Returns q_out, or (q_out, k_out)."""
-    dtype, shape = q.dtype, q.shape
+    shape = q.shape
     dims = len(shape)
-    if dims not in (3, 4) or dtype not in DTYPES:
+    dtype = DTYPES.get(q.dtype)
+    if dtype is None or dims not in (3, 4):
         raise ValueError("q must be [B, heads, N, D] or [heads, N, D] in bf16, fp16 or fp32")
     dev = _device(q, "q")
-    N, D = shape[-2:]
+    heads, N, D = shape[-3:]
     B = shape[0] if dims == 4 else 1
-    if grid is None:
-        if pos is None or flat_in or flat_out:
-            raise ValueError("grid is needed without pos and for a flattened order")
-        grid = (N, 1, 1)
-    T, H, W = grid
-    if T * H * W != N:
-        raise ValueError("grid %s does not hold %d tokens" % (tuple(grid), N))
-    views, heads, results = [b"", b""], [0, 0], []
-    for i, (x, y) in enumerate(((q, q_out), (k, k_out))):
-        if x is None:
-            break
-        if i and (x.shape[-2:] != shape[-2:] or x.dim() != dims or (dims == 4 and x.shape[0] != B)):
+    if grid is not None:
+        T, H, W = grid
+        if T * H * W != N:
+            raise ValueError("grid %s does not hold %d tokens" % (tuple(grid), N))
+    elif pos is None or flat_in or flat_out:
+        raise ValueError("grid is needed without pos and for a flattened order")
+    else:
+        T, H, W = N, 1, 1
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    ins, outs = _rope_view(q, q, shape, dev), _rope_view(q_out, q, shape, dev)
+    heads_k = 0
+    if k is not None:
+        shape_k = k.shape
+        heads_k = shape_k[-3]
+        if len(shape_k) != dims or shape_k[-2:] != (N, D) or (dims == 4 and shape_k[0] != B):
             raise ValueError("q and k must have the same batch, tokens and D")
-        if y is None:
-            y = torch.empty_like(x)
-        elif y.shape != x.shape:
-            raise ValueError("an output must have its input's shape")
-        results.append(y)
-        heads[i] = x.shape[-3]
-        for side, t in ((0, x), (1, y)):
-            s = t.stride()
-            if t.dtype != dtype or t.get_device() != dev or (s[-1] != 1 and D > 1):
-                raise ValueError("q, k and the outputs must be %s tensors on cuda:%d with contiguous rows"
-                                 % (dtype, dev))
-            views[side] += _VIEW(t.data_ptr(), s[0] if dims == 4 else 0, s[-3], s[-2])
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        ins += _rope_view(k, q, shape_k, dev)
+        outs += _rope_view(k_out, q, shape_k, dev)
     pos_ptr, pos_batch, axes = None, 0, 0
     if pos is not None:
         axes = pos.shape[-1]
         pos_ptr = _int32(pos, "pos", dev, (N, axes) if pos.dim() == 2 else (B, N, axes))
         pos_batch = N * axes if pos.dim() == 3 else 0
     p = RopeParams.from_buffer_copy(params)
-    p.dtype, p.D = DTYPES[dtype], D
-    p.flags |= (ROPE_FLAT_IN if flat_in else 0) | (ROPE_FLAT_OUT if flat_out else 0)
-    _call(lib().nabla_rope, "nabla_rope", dev, ctypes.byref(p), B, T, H, W, P, len(results),
-          struct.pack("@ii", *heads), views[0], views[1], pos_ptr, pos_batch, axes)
-    return results[0] if k is None else tuple(results)
+    p.dtype, p.D = dtype, D
+    if flat_in or flat_out:
+        p.flags |= (ROPE_FLAT_IN if flat_in else 0) | (ROPE_FLAT_OUT if flat_out else 0)
+    _call(lib().nabla_rope, "nabla_rope", dev, ctypes.byref(p), B, T, H, W, P, 1 if k is None else 2,
+          _HEADS(heads, heads_k), ins, outs, pos_ptr, pos_batch, axes)
+    return q_out if k is None else (q_out, k_out)
+
+
+def _rope_view(t, q, shape, dev):
+    """nabla_view of [heads, N, D] or [B, heads, N, D] in q's type."""
+    s = t.stride()
+    if t.dtype != q.dtype or t.get_device() != dev or t.shape != shape or s[-1] != 1 != shape[-1]:
+        raise ValueError("q, k and their outputs must be %s tensors on cuda:%d with contiguous rows, "
+                         "outputs in their inputs' shapes" % (q.dtype, dev))
+    return _VIEW(t.data_ptr(), 0, s[0], s[1]) if len(s) == 3 else _VIEW(t.data_ptr(), *s[:3])
 
 
 def _packed_of(q, k, cu_q, causal, scale):
