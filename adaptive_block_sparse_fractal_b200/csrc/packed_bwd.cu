@@ -934,7 +934,9 @@ static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_til
     using namespace nabla::packed;
     cudaError_t err;
     if (a.total_q > 0) {
-        const int per = 2;  // heads a CTA of pre_kernel: 24 us at 100 MB; 8 a CTA took 38
+        // heads a CTA of pre_kernel: 2 take 24 us at 100 MB, 1 27, 8 38; one where two
+        // would not fill the GPU (six CTAs an SM)
+        const int per = q_tiles * a.heads > 2 * 6 * kSms ? 2 : 1;
         pre_kernel<D><<<dim3(static_cast<unsigned>(q_tiles), (a.heads + per - 1) / per), kPreThreads, 0,
                         stream>>>(a, per);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
