@@ -21,9 +21,19 @@
 // float32.  MMAs go out four per elect.sync from converged warps (an N = 64 MMA
 // is accepted about when it starts, so the issuer must not fall behind).
 //
+// delta = dout . o takes o as it was rounded to bf16.  With many keys that is small
+// against the rounding of dS; with few, dP - delta cancels and the rounding of o
+// stays: over sequences of 3 rows the gradients were off by 0.5%, of 2 rows by 3%.
+// So where one tile holds all keys of a row, delta is the sum over that tile of P
+// dP in float32, the same number unrounded: in dkdv for sequences of at most 64
+// keys, in dq for rows that keep at most 64.  (Taking o again from q, k and v in
+// pre_kernel instead cost 96 us for 4,096 rows and 24 heads on 30 keys.)
+//
 // Rows behind a sequence inside a tile: scores are replaced by -inf, and rows
 // that are summed over (Q and dO in dkdv, K in dq) are zeroed in shared memory,
 // as 0 * NaN would spread.  Waits are bounded as in the forward.
+#include <type_traits>
+
 #include "packed.cuh"
 
 namespace nabla {
@@ -37,105 +47,10 @@ constexpr int kPreThreads = 256;
 // ---------------------------------------------------------------------------
 // delta and lse, padded: one CTA per 64 rows of a sequence and `per` heads
 // ---------------------------------------------------------------------------
-// delta = dout . o takes o as it was rounded to bf16.  With many keys that is
-// small against the rounding of dS; with few, dP - delta cancels and the rounding
-// of o stays: over sequences of 3 rows the gradients were off by 0.5%, of 2 rows
-// by 3%.  Tiles whose rows keep at most this many keys take o again in float32
-// (P as two bf16 terms, 2^-17), which brings them to the 0.23% of long ones.
-// (Up to 128 keys would cost 290 us in a cross attention of 3,000 rows and 24 heads
-// to 77 keys, to go from 0.28% to 0.23%.)
-constexpr int kFewKeys = 32;
-
-// dout . o of 64 rows of head h over kmax <= kFewKeys keys, each half of the
-// features by four warps of 16 rows (m16n8k16, operands straight from global
-// memory: few tiles take this path, or few keys are there to read).
 template <int D>
-__device__ __forceinline__ void exact_delta(const Args &a, const SeqTile &st, int h, int kmax, float (*part)[64]) {
-    constexpr int kN = D / 16;  // 8-feature tiles of a half
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rg = warp & 3, half = warp >> 2;
-    const int hk = h / a.group, off = st.Lk - st.Lq;
-    const int col = 2 * (lane & 3), sub = lane >> 2;
-    int row[2];
-    const __nv_bfloat16 *q[2], *g[2];
-    float nl[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        row[e] = st.tile * 64 + rg * 16 + sub + 8 * e;
-        const int64_t tok = st.q0 + min(row[e], st.Lq - 1);
-        q[e] = a.q.row(tok, h) + col;
-        g[e] = a.dout.row(tok, h) + half * (D / 2) + col;
-        nl[e] = -(a.lse[h * a.total_q + tok] * 1.4426950408889634f);
-    }
-    float acc[kN][4] = {};
-    for (int kb = 0; kb < kmax; kb += 16) {
-        float s[2][4] = {};
-#pragma unroll 4
-        for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t qa[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                qa[e] = __ldg(reinterpret_cast<const uint32_t *>(q[e & 1] + 16 * kk + 8 * (e >> 1)));
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const __nv_bfloat16 *k = a.k.row(st.k0 + min(kb + 8 * n + sub, st.Lk - 1), hk) + 16 * kk + col;
-                mma_bf16(s[n], qa, __ldg(reinterpret_cast<const uint32_t *>(k)),
-                         __ldg(reinterpret_cast<const uint32_t *>(k + 8)));
-            }
-        }
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {  // operand register: row x & 1, keys 8 (x >> 1) + col, + 1
-            float p[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int key = kb + 8 * (x >> 1) + col + e;
-                const bool keep = key < st.Lk && (!a.causal || key <= row[x & 1] + off);
-                p[e] = keep ? fast_exp2(fmaf(s[x >> 1][2 * (x & 1) + e], a.c, nl[x & 1])) : 0.f;
-            }
-            hi[x] = pack_bf16(p[0], p[1]);
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&hi[x]));
-            lo[x] = pack_bf16(p[0] - f.x, p[1] - f.y);
-        }
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-            uint32_t b[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t pair = 0;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int key = kb + 8 * x + col + e;
-                    if (key < st.Lk)
-                        pair |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(
-                                    a.v.row(st.k0 + key, hk) + half * (D / 2) + 8 * n + sub))) << (16 * e);
-                }
-                b[x] = pair;
-            }
-            mma_bf16(acc[n], hi, b[0], b[1]);
-            mma_bf16(acc[n], lo, b[0], b[1]);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        float d = 0.f;
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(g[e] + 8 * n));
-            d = fmaf(acc[n][2 * e], f.x, d);
-            d = fmaf(acc[n][2 * e + 1], f.y, d);
-        }
-        d += __shfl_xor_sync(0xffffffffu, d, 1);
-        d += __shfl_xor_sync(0xffffffffu, d, 2);
-        if ((lane & 3) == 0) part[half][rg * 16 + sub + 8 * e] = d;
-    }
-}
-
-template <int D>
-__global__ void __launch_bounds__(kPreThreads, 6) pre_kernel(const __grid_constant__ Args a, int per) {
+__global__ void __launch_bounds__(kPreThreads) pre_kernel(const __grid_constant__ Args a, int per) {
     __shared__ SeqTile st;
     __shared__ int64_t sums[kPreThreads / 32];
-    __shared__ float part[2][64];
     allow_dependents();
     if (!find_seq<kPreThreads>(a, blockIdx.x, [](int Lq, int) { return (Lq + 63) >> 6; }, &st, sums))
         return;
@@ -143,22 +58,8 @@ __global__ void __launch_bounds__(kPreThreads, 6) pre_kernel(const __grid_consta
     constexpr int kStep = kPreThreads / TPR;
     const int sub = threadIdx.x % TPR;
     const int h1 = min(a.heads, static_cast<int>(blockIdx.y + 1) * per);
-    const int last = min(st.tile * 64 + 63, st.Lq - 1);
-    const int kmax = a.causal ? min(st.Lk, last + 1 + st.Lk - st.Lq) : st.Lk;  // keys of the tile's last row
     for (int h = blockIdx.y * per; h < h1; ++h) {
         const int64_t base = h * a.pad_rows + static_cast<int64_t>(st.pad + st.tile) * 64;
-        if (kmax > 0 && kmax <= kFewKeys) {
-            exact_delta<D>(a, st, h, kmax, part);
-            __syncthreads();
-            if (threadIdx.x < 64) {
-                const int r = threadIdx.x, i = st.tile * 64 + r;
-                const float L = i < st.Lq ? a.lse[h * a.total_q + st.q0 + i] : -INFINITY;
-                a.pad_d[base + r] = L == -INFINITY ? 0.f : -(part[0][r] + part[1][r]);
-                a.pad_l[base + r] = L == -INFINITY ? -INFINITY : -(L * 1.4426950408889634f);
-            }
-            __syncthreads();
-            continue;
-        }
 #pragma unroll
         for (int r = threadIdx.x / TPR; r < 64; r += kStep) {
             const int i = st.tile * 64 + r;
@@ -201,7 +102,8 @@ struct KvLayout {
     static constexpr uint32_t KV_RING = kHalves * kHalfTile;
     static constexpr uint32_t KV_BAR = KV_RING + kStages * kStageBytes;
     static constexpr int kBars = 1 + 2 * kStages + 2 + 2 + 1 + 1 + 1 + 1;
-    static constexpr uint32_t KV_SEQ = KV_BAR + 8 * kBars;
+    static constexpr uint32_t KV_COL = (KV_BAR + 8 * kBars + 15) / 16 * 16;  // sums over keys: [2][2][64]
+    static constexpr uint32_t KV_SEQ = KV_COL + 2 * 2 * 64 * 4;
     static constexpr uint32_t KV_SUM = (KV_SEQ + sizeof(SeqTile) + 7) / 8 * 8;
     static constexpr uint32_t KV_INT = KV_SUM + 8 * (kKvThreads / 32);
     static constexpr uint32_t kSmem = KV_INT + 16 + 1024;
@@ -428,8 +330,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         const float c = a.c;
         const uint64_t c2 = f2_pack(c, c);
         const int nt = *abort_flag ? 0 : ntiles;
+        float *col = reinterpret_cast<float *>(sm + L::KV_COL);
         int qt = qs;  // query tile within its head
-        for (int t = 0; t < nt; ++t) {
+        auto tile = [&](int t, auto few) {
             ok = wait_bar(&s_full[t & 1], (t >> 1) & 1, abort_flag, a.status, a.limit) && ok;
             tc_fence_after();
             const uint32_t scol = tmem + lane_base + (t & 1) * 64 + 32 * qg;
@@ -451,20 +354,59 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) sv[e] = e >= first ? sv[e] : -INFINITY;
             }
+            if constexpr (few.value) {
+                // P, then delta as the sum of P dP over the keys: lanes and two warps
 #pragma unroll
-            for (int q4 = 0; q4 < 8; ++q4) {
-                const float4 l4 = L4[q4], d4 = D4[q4];
-                const float la[4] = {l4.x, l4.y, l4.z, l4.w};
-                const float da[4] = {d4.x, d4.y, d4.z, d4.w};
+                for (int q4 = 0; q4 < 8; ++q4) {
+                    const float4 l4 = L4[q4];
+                    const float la[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const int q = 4 * q4 + e;
-                    const uint64_t x = f2_fma(f2_pack(sv[q], sv[q + 1]), c2, f2_pack(la[e], la[e + 1]));
-                    const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
-                    const uint64_t g = f2_mul(f2_pack(p0, p1),
-                                              f2_add(f2_pack(dp[q], dp[q + 1]), f2_pack(da[e], da[e + 1])));
-                    pk[2 * q4 + (e >> 1)] = pack_bf16(p0, p1);
-                    dk2[2 * q4 + (e >> 1)] = pack_bf16(f2_lo(g), f2_hi(g));
+                    for (int e = 0; e < 4; ++e) sv[4 * q4 + e] = fast_exp2(fmaf(sv[4 * q4 + e], c, la[e]));
+                }
+                float v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = key < Lk ? sv[e] * dp[e] : 0.f;
+                // 32 values of 32 lanes: lane l ends with the sum of value l
+#pragma unroll
+                for (int h = 16; h; h >>= 1) {
+                    const bool up = lane & h;
+#pragma unroll
+                    for (int i = 0; i < h; ++i) {
+                        const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + h], h);
+                        v[i] = (up ? v[i + h] : v[i]) + other;
+                    }
+                }
+                float *sum = col + (t & 1) * 128;  // (two buffers: one barrier a tile)
+                if (wq < 2) sum[64 * wq + 32 * qg + lane] = v[0];
+                bar_sync(1 + qg, 128);
+                const float4 *A4 = reinterpret_cast<const float4 *>(sum + 32 * qg);
+#pragma unroll
+                for (int q4 = 0; q4 < 8; ++q4) {
+                    const float4 x = A4[q4], y = A4[q4 + 16];
+                    const float d[4] = {x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const int q = 4 * q4 + e;
+                        pk[q >> 1] = pack_bf16(sv[q], sv[q + 1]);
+                        dk2[q >> 1] = pack_bf16(sv[q] * (dp[q] - d[e]), sv[q + 1] * (dp[q + 1] - d[e + 1]));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int q4 = 0; q4 < 8; ++q4) {
+                    const float4 l4 = L4[q4], d4 = D4[q4];
+                    const float la[4] = {l4.x, l4.y, l4.z, l4.w};
+                    const float da[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const int q = 4 * q4 + e;
+                        const uint64_t x = f2_fma(f2_pack(sv[q], sv[q + 1]), c2, f2_pack(la[e], la[e + 1]));
+                        const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
+                        const uint64_t g = f2_mul(f2_pack(p0, p1),
+                                                  f2_add(f2_pack(dp[q], dp[q + 1]), f2_pack(da[e], da[e + 1])));
+                        pk[2 * q4 + (e >> 1)] = pack_bf16(p0, p1);
+                        dk2[2 * q4 + (e >> 1)] = pack_bf16(f2_lo(g), f2_hi(g));
+                    }
                 }
             }
             tmem_st16(scol, pk);
@@ -474,7 +416,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&pd_full[t & 1]);
             if (++qt == qs + per) qt = qs;
-        }
+        };
+        if (Lk <= 64)  // all keys of the sequence are in this tile's first rows
+            for (int t = 0; t < nt; ++t) tile(t, std::true_type{});
+        else
+            for (int t = 0; t < nt; ++t) tile(t, std::false_type{});
         if (ok && nt > 0) ok = wait_bar(done, 0, abort_flag, a.status, a.limit);
         tc_fence_after();
         // warp-uniform flags around the collective TMEM loads
@@ -545,8 +491,9 @@ struct DqLayout {
     static constexpr uint32_t kBlockBytes = 64u * D * 2;  // 64 keys of K or V
     static constexpr uint32_t kDqSlot = 2 * kBlockBytes;
     static constexpr uint32_t DQ_STAGE = kDqRing * kDqSlot;  // 2 KB per dS warp
-    static constexpr uint32_t DQ_BAR = DQ_STAGE + 8 * 2048;
-    static constexpr int kBars = 2 * kDqRing + 2 + 2 + 1 + 1 + 2 + 1 + 1 + 4;
+    static constexpr uint32_t DQ_RED = DQ_STAGE + 8 * 2048;  // sums over the keys of a half: [2][128]
+    static constexpr uint32_t DQ_BAR = DQ_RED + 2 * 128 * 4;
+    static constexpr int kBars = 2 * kDqRing + 2 + 2 + 1 + 1 + 2 + 1 + 1 + 4 + 4;
     static constexpr uint32_t DQ_UNIT = DQ_BAR + 8 * kBars;
     static constexpr uint32_t DQ_INT = (DQ_UNIT + 2 * sizeof(DqUnit) + 15) / 16 * 16;
     static constexpr uint32_t kSmem = DQ_INT + 16 + 1024;
@@ -571,6 +518,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     uint64_t *ds_full = s_full + 2, *q_ready = ds_full + 2, *done = q_ready + 1;
     uint64_t *s_free = done + 1, *sdp_done = s_free + 2, *raw_full = sdp_done + 1;
     uint64_t *u_full = raw_full + 1, *u_empty = u_full + 2;  // per unit slot; read by ten warps
+    uint64_t *pair = u_empty + 2;  // the two dS warps that share rows
     volatile DqUnit *units = reinterpret_cast<DqUnit *>(sm + L::DQ_UNIT);
     int *sInt = reinterpret_cast<int *>(sm + L::DQ_INT);  // [0] tmem base [2] abort
     volatile int *abort_flag = sInt + 2;
@@ -595,6 +543,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             mbar_init(&u_full[b], 1);
             mbar_init(&u_empty[b], 10);
         }
+        for (int w = 0; w < 4; ++w) mbar_init(&pair[w], 2);
         sInt[2] = *reinterpret_cast<volatile int *>(a.status) != 0 ? 1 : 0;
         fence_mbar_init();
     }
@@ -607,7 +556,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const bool go = !__syncthreads_or(!good);
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(sInt[0]);
-    bool ok = go && __all_sync(0xffffffffu, *abort_flag == 0);
+    bool ok = go && sInt[2] == 0;  // set in front of the barrier: the same in all threads
 
     if (warp == 0) {
         // ---------------- producer: units, then their K and V tiles through the ring ----------------
@@ -823,7 +772,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             return __all_sync(0xffffffffu, wait_bar(&u_full[n & 1], (n >> 1) & 1u, abort_flag, a.status, a.limit));
         };
         int b = 0;
-        uint32_t phase = 0, ended = 0;
+        uint32_t phase = 0, ended = 0, singles = 0;
         ok = ok && arrived(0);
         if (ok && units[0].valid && units[0].nt > 0) fetch(0);
         for (uint32_t n = 0; ok; ++n) {
@@ -848,7 +797,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_ready);
             }
-            for (int t = 0; t < nt; ++t, left -= 64, left0 -= 64) {
+            // (two instances: the test for a single tile inside the loop cost it 8%)
+            auto tile = [&](auto only) {
                 ok = wait_bar(&s_full[b], phase, abort_flag, a.status, a.limit) && ok;
                 tc_fence_after();
                 const uint32_t scol = tmem + lane_base + b * 64 + 32 * kg;
@@ -864,12 +814,32 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                         dp[e] = e <= left ? dp[e] : 0.f;
                     }
                 }
+                if constexpr (only.value) {
+                    // the only tile: delta is the sum of P dP over it
+                    float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const uint64_t x = f2_fma(f2_pack(sv[e], sv[e + 1]), c2, nl2);
-                    const uint64_t g = f2_mul(f2_pack(fast_exp2(f2_lo(x)), fast_exp2(f2_hi(x))),
-                                              f2_add(f2_pack(dp[e], dp[e + 1]), nd2));
-                    gk[e >> 1] = pack_bf16(f2_lo(g), f2_hi(g));
+                    for (int e = 0; e < 32; ++e) {
+                        sv[e] = fast_exp2(fmaf(sv[e], a.c, nLr));
+                        sum = fmaf(sv[e], dp[e], sum);
+                    }
+                    float *red = reinterpret_cast<float *>(sm + L::DQ_RED);
+                    red[128 * kg + r] = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pair[wq]);
+                    // (bounded, as every wait; the next write is behind the next unit's q_ready)
+                    ok = wait_bar(&pair[wq], singles++ & 1u, abort_flag, a.status, a.limit) && ok;
+                    sum += red[128 * (kg ^ 1) + r];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        gk[e >> 1] = pack_bf16(sv[e] * (dp[e] - sum), sv[e + 1] * (dp[e + 1] - sum));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const uint64_t x = f2_fma(f2_pack(sv[e], sv[e + 1]), c2, nl2);
+                        const uint64_t g = f2_mul(f2_pack(fast_exp2(f2_lo(x)), fast_exp2(f2_hi(x))),
+                                                  f2_add(f2_pack(dp[e], dp[e + 1]), nd2));
+                        gk[e >> 1] = pack_bf16(f2_lo(g), f2_hi(g));
+                    }
                 }
                 // bf16 dS of keys [32 kg, 32 kg + 32) over this group's first 16 S columns
                 tmem_st16(scol, gk);
@@ -881,7 +851,13 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                     b = 0;
                     phase ^= 1u;
                 }
-            }
+                left -= 64;
+                left0 -= 64;
+            };
+            if (nt == 1)
+                tile(std::true_type{});
+            else
+                for (int t = 0; t < nt; ++t) tile(std::false_type{});
             // the next unit's rows travel while this one ends
             ok = ok && arrived(n + 1);
             ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);

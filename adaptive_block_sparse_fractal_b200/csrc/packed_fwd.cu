@@ -508,10 +508,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float c = a.c;
         const uint64_t c2 = f2_pack(c, c);
         uint32_t ns = 0;  // tiles this row tile has seen
-        bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
+        bool ok = true;
+        // The two warps that share rows meet at named barriers, so they go on or give
+        // up together.
+        auto both = [&](bool good) -> bool { return !bar_or(pair, 64, !good || *abort_flag != 0); };
         for (uint32_t n = 0; ok; ++n) {
             const int us = n & 1;
-            ok = __all_sync(0xffffffffu, wait_bar(&u_full[us], (n >> 1) & 1u, abort_flag, a.status, a.limit));
+            ok = both(wait_bar(&u_full[us], (n >> 1) & 1u, abort_flag, a.status, a.limit));
             if (!ok) break;
             const volatile Unit &u = units[us];
             if (!u.valid) break;
@@ -618,11 +621,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 red[128 * h] = l;
                 again = bar_or(pair, 64, over);  // (and the sums are exchanged)
                 l += red[128 * (h ^ 1)];
-                bar_sync(pair, 64);  // read by both before the next unit's maxima
                 if (again && lane == 0) units[us].redo = 1;
             }
             tc_fence_after();
-            ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+            ok = both(ok);  // (and the sums are read before the next unit's maxima)
             if (!ok) break;
             const int head = u.hk * G + rh;
             const int64_t grow = u.q0 + tok;

@@ -308,7 +308,8 @@ def test_forward_scores_that_jump_far_above_the_first_tile(D, step):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("lens_q,lens_k,causal", [([2] * 40, [2] * 40, True), ([3, 2, 1, 4] * 8, [3, 2, 1, 4] * 8, True),
                                                   ([70, 9], [2, 3], False), ([20, 31], [20, 31], True),
-                                                  ([200, 64], [32, 17], False)])
+                                                  ([200, 64], [32, 17], False), ([60, 64, 1], [60, 64, 1], True),
+                                                  ([130, 3], [64, 33], False), ([90], [20], True)])
 def test_gradients_with_few_keys(lens_q, lens_k, causal, D):
     """Few keys: dP - delta cancels, so delta must not carry the rounding of o.
     The bound without that term: dS is rounded to bf16 once (h |dS|), and P (dP -
@@ -325,7 +326,7 @@ def test_gradients_with_few_keys(lens_q, lens_k, causal, D):
             keep = seq_util.keep_mask(b - a, e - c, causal, "cuda")
             x = seq_util.attention(Q, K, V, sc, keep, G)
             p = ((Q @ K.T) * sc).masked_fill(~keep, -math.inf)
-            p = torch.softmax(p, 1)
+            p = torch.where(keep, torch.softmax(p, 1), torch.zeros_like(p))  # (a row that keeps nothing has p = 0)
             dp = G @ V.T
             ds = p * (dp - (G * x["o"]).sum(1, keepdim=True))
             dds = h * ds.abs() + seq_util.E * p * (G.abs() @ V.abs().T + (G * x["o"]).abs().sum(1, keepdim=True))
