@@ -359,7 +359,7 @@ int nabla_rope(const nabla_rope_params *params, int B, int T, int H, int W, int 
  * Borders that do not ascend, or that leave [0, total], make the call write
  * NABLA_ERR_PARAM to the workspace status and leave the outputs unwritten.
  * NaN and infinities in rows of other sequences, or of none, never reach a
- * sequence.  Inside one, a NaN or infinity of a row of v (backward: of q or dout)
+ * sequence.  Inside one, a row that keeps a key of score NaN or +infinity is NaN; a NaN or infinity of a row of v (backward: of q or dout)
  * can also reach the rows of the same tile of up to 128 that mask it (causal).
  * A workspace serves one call at a time. */
 typedef struct {
