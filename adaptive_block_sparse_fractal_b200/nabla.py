@@ -386,13 +386,15 @@ def rope_params_of(pairs, theta=10000.0, scale=1.0, offset=0.0, layout=ROPE_ADJA
     if not 1 <= len(pairs) <= 3:
         raise ValueError("pairs: one to three axes")
 
-    def axes(x):
+    def axes(x, name):
         x = [float(v) for v in x] if isinstance(x, (tuple, list)) else [float(x)] * len(pairs)
-        return tuple(x[:3]) + (1.0,) * (3 - len(x[:3]))
+        if len(x) != len(pairs):
+            raise ValueError("%s: one number, or one for each of the %d axes" % (name, len(pairs)))
+        return tuple(x) + (1.0,) * (3 - len(x))  # (axes without pairs are not looked at)
     p = RopeParams()
     p.layout = int(layout)
     p.pairs = tuple(pairs) + (0,) * (3 - len(pairs))
-    p.theta, p.scale, p.offset = axes(theta), axes(scale), axes(offset)
+    p.theta, p.scale, p.offset = axes(theta, "theta"), axes(scale, "scale"), axes(offset, "offset")
     p.flags = ROPE_INVERSE if inverse else 0
     return p
 
