@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         mbar_init(k_ready, 8);
         mbar_init(dp_free, 8);
         mbar_init(raw_full, 1);
-        sInt[2] = *reinterpret_cast<volatile int *>(a.status) != 0 ? 1 : 0;
+        sInt[2] = sInt[3] = *reinterpret_cast<volatile int *>(a.status) != 0 ? 1 : 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -329,7 +329,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         if (lane == 0) mbar_arrive(k_ready);
         const float c = a.c;
         const uint64_t c2 = f2_pack(c, c);
-        const int nt = *abort_flag ? 0 : ntiles;
+        // (sInt[3] does not change, unlike the abort flag: the warps that meet at the
+        // barriers of a tile below agree on their number)
+        const int nt = sInt[3] != 0 ? 0 : ntiles;
         float *col = reinterpret_cast<float *>(sm + L::KV_COL);
         int qt = qs;  // query tile within its head
         auto tile = [&](int t, auto few) {
