@@ -187,7 +187,8 @@ int check_packed(const nabla_packed *s, const int32_t *cu_q, const int32_t *cu_k
                  size_t bytes) {
     if (s == nullptr) return NABLA_ERR_NULL;
     if (!packed_shape_ok(s)) return NABLA_ERR_SHAPE;
-    if (!(s->scale > 0.f) || !std::isfinite(s->scale) || (s->causal != 0 && s->causal != 1))
+    if (!(s->scale > 0.f) || !std::isfinite(s->scale) ||
+        (s->causal & ~static_cast<int>(1u | NABLA_DEBUG_TIMEOUT)) != 0)
         return NABLA_ERR_PARAM;
     if (cu_q == nullptr || cu_k == nullptr) return NABLA_ERR_NULL;
     if (!aligned4(cu_q) || !aligned4(cu_k)) return NABLA_ERR_ALIGN;
@@ -206,12 +207,13 @@ nabla::packed::Args packed_args(const nabla_packed *s, const int32_t *cu_q, cons
     a.heads = s->heads;
     a.heads_kv = s->heads_kv;
     a.group = s->heads / s->heads_kv;
-    a.causal = s->causal;
+    a.causal = s->causal & 1;
     a.tile_tokens = tile_tokens(s);
     a.splits = 1;
     a.c = s->scale * 1.4426950408889634f;
     a.scale = s->scale;
-    a.limit = 1000000000u;  // 1 s per wait
+    a.stall = (s->causal & NABLA_DEBUG_TIMEOUT) != 0;
+    a.limit = a.stall ? 1000000u : 1000000000u;  // 1 s per wait (1 ms when it is to expire)
     return a;
 }
 

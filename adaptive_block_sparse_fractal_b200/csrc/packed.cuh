@@ -30,6 +30,7 @@ struct Args {
     int tile_tokens, splits;  // forward: tokens a row tile (128 / group), splits of the key range
     float c, scale;    // scale * log2(e), scale
     uint32_t limit;    // ns per wait
+    int stall;         // test aid: no keys (dK, dV: no queries) are loaded, so that the waits for them expire
 };
 
 struct SeqTile {

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
                 for (int h = 0; h < kHalves; ++h)
                     tma_load_3d(sb + KV_V + h * kHalfTile, &tv, kv_full, 64 * h, hk, st->k0 + j0);
             }
-            for (; t < ntiles; ++t) {
+            for (; t < ntiles && !a.stall; ++t) {
                 const int s = t % kStages, g = t / per, i0 = (qs + t % per) * 64;
                 const bool ok = __all_sync(
                     0xffffffffu, lane != 0 || wait_bar(&st_empty[s], ((t / kStages) & 1) ^ 1,
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             mbar_init(&u_empty[b], 10);
         }
         for (int w = 0; w < 4; ++w) mbar_init(&pair[w], 2);
-        sInt[2] = *reinterpret_cast<volatile int *>(a.status) != 0 ? 1 : 0;
+        sInt[2] = sInt[3] = *reinterpret_cast<volatile int *>(a.status) != 0 ? 1 : 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const bool go = !__syncthreads_or(!good);
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(sInt[0]);
-    bool ok = go && sInt[2] == 0;  // set in front of the barrier: the same in all threads
+    bool ok = go && sInt[3] == 0;  // (not the abort flag: the same in all threads)
 
     if (warp == 0) {
         // ---------------- producer: units, then their K and V tiles through the ring ----------------
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 mbar_arrive(&u_full[us]);
             }
             __syncwarp();
-            if (!u.valid) break;
+            if (!u.valid || a.stall) break;
             for (int t = 0; ok && t < u.nt; ++t) {
                 const int slot = seq % kDqRing;
                 ok = __all_sync(0xffffffffu, lane != 0 || wait_bar(&kv_empty[slot], ((seq / kDqRing) & 1u) ^ 1u,
@@ -861,6 +861,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             else
                 for (int t = 0; t < nt; ++t) tile(std::false_type{});
             // the next unit's rows travel while this one ends
+            ok = __all_sync(0xffffffffu, ok);  // (lanes may have given up apart; the vote in `arrived` is the warp's)
             ok = ok && arrived(n + 1);
             ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
             if (!ok) break;

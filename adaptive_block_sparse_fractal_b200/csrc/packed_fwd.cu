@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (!ok) break;
+                if (!ok || a.stall) break;
                 load(u, &tk, u.j0, false);
                 for (int i = 1; ok && i < emax; ++i) {
                     load(u, &tv, u.j0 + i - 1, true);

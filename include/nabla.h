@@ -65,8 +65,9 @@ typedef struct CUstream_st *nabla_stream_t; /* == cudaStream_t */
  * depends on the scores (0 < p < 1 and not NABLA_FULL_STA). */
 #define NABLA_DEBUG_SCORES 8u
 /* Test aid, not for production: makes the tensor-core attention forward and
- * backward, and the persistent front end of nabla_build_mask_grid, give up a
- * device-side wait at once (or after 1 ms), so that the timeout path (status
+ * backward, the persistent front end of nabla_build_mask_grid, and (or-ed into
+ * nabla_packed.causal) the packed calls give up a device-side wait at once (or
+ * after 1 ms), so that the timeout path (status
  * word = NABLA_ERR_TIMEOUT, clean unwind, context still usable) can be
  * exercised without faulting or hanging the GPU.  Outputs are not meaningful
  * after it. */
