@@ -24,10 +24,10 @@
 // delta = dout . o takes o as it was rounded to bf16.  With many keys that is small
 // against the rounding of dS; with few, dP - delta cancels and the rounding of o
 // stays: over sequences of 3 rows the gradients were off by 0.5%, of 2 rows by 3%.
-// So where one tile holds all keys of a row, delta is the sum over that tile of P
-// dP in float32, the same number unrounded: in dkdv for sequences of at most 64
-// keys, in dq for rows that keep at most 64.  (Taking o again from q, k and v in
-// pre_kernel instead cost 96 us for 4,096 rows and 24 heads on 30 keys.)
+// So for every row that keeps at most 64 keys -- all of them in the first tile of its
+// sequence, whatever else the row's tile or unit holds -- delta is the sum over
+// that tile of P dP in float32, the same number unrounded.  (Taking o again from q, k
+// and v in pre_kernel instead cost 96 us for 4,096 rows and 24 heads on 30 keys.)
 //
 // Rows behind a sequence inside a tile: scores are replaced by -inf, and rows
 // that are summed over (Q and dO in dkdv, K in dq) are zeroed in shared memory,
@@ -334,6 +334,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         const int nt = sInt[3] != 0 ? 0 : ntiles;
         float *col = reinterpret_cast<float *>(sm + L::KV_COL);
         int qt = qs;  // query tile within its head
+        // queries in front of `few_end` keep at most 64 keys, all in this tile
+        const int few_end = Lk <= 64 ? Lq : a.causal && j0 == 0 ? max(0, min(Lq, 64 - off)) : 0;
         auto tile = [&](int t, auto few) {
             ok = wait_bar(&s_full[t & 1], (t >> 1) & 1, abort_flag, a.status, a.limit) && ok;
             tc_fence_after();
@@ -354,10 +356,14 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             const int first = a.causal ? key - off - qt * 64 - 32 * qg : 0;
             if (a.causal && j0 + 127 - off > qt * 64 + 32 * qg) {  // uniform: the tile is masked
 #pragma unroll
-                for (int e = 0; e < 32; ++e) sv[e] = e >= first ? sv[e] : -INFINITY;
+                for (int e = 0; e < 32; ++e) {
+                    sv[e] = e >= first ? sv[e] : -INFINITY;
+                    if constexpr (few.value) dp[e] = e >= first ? dp[e] : 0.f;
+                }
             }
             if constexpr (few.value) {
                 // P, then delta as the sum of P dP over the keys: lanes and two warps
+                // (the first 64 keys, all that such a query keeps)
 #pragma unroll
                 for (int q4 = 0; q4 < 8; ++q4) {
                     const float4 l4 = L4[q4];
@@ -365,21 +371,32 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sv[4 * q4 + e] = fast_exp2(fmaf(sv[4 * q4 + e], c, la[e]));
                 }
-                float v[32];
+                const int end = few_end - qt * 64 - 32 * qg;  // of this group's 32 queries
+                float mine = 0.f;
+                if (end > 0) {
+                    float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = key < Lk ? sv[e] * dp[e] : 0.f;
-                // 32 values of 32 lanes: lane l ends with the sum of value l
+                    for (int e = 0; e < 32; ++e) v[e] = key < Lk ? sv[e] * dp[e] : 0.f;
+                    // 32 values of 32 lanes: lane l ends with the sum of value l
 #pragma unroll
-                for (int h = 16; h; h >>= 1) {
-                    const bool up = lane & h;
+                    for (int h = 16; h; h >>= 1) {
+                        const bool up = lane & h;
 #pragma unroll
-                    for (int i = 0; i < h; ++i) {
-                        const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + h], h);
-                        v[i] = (up ? v[i + h] : v[i]) + other;
+                        for (int i = 0; i < h; ++i) {
+                            const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + h], h);
+                            v[i] = (up ? v[i + h] : v[i]) + other;
+                        }
                     }
+                    mine = v[0];
                 }
-                float *sum = col + (t & 1) * 128;  // (two buffers: one barrier a tile)
-                if (wq < 2) sum[64 * wq + 32 * qg + lane] = v[0];
+                // (two buffers, one barrier a tile: S^T of tile t + 2 is issued behind the
+                // arrival on pd_full that ends tile t in every warp)
+                float *sum = col + (t & 1) * 128;
+                if (wq < 2) {
+                    // a query that keeps more takes the delta of pre_kernel
+                    if (lane >= end) mine = wq == 0 ? -reinterpret_cast<const float *>(D4)[lane] : 0.f;
+                    sum[64 * wq + 32 * qg + lane] = mine;
+                }
                 bar_sync(1 + qg, 128);
                 const float4 *A4 = reinterpret_cast<const float4 *>(sum + 32 * qg);
 #pragma unroll
@@ -419,7 +436,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
             if (lane == 0) mbar_arrive(&pd_full[t & 1]);
             if (++qt == qs + per) qt = qs;
         };
-        if (Lk <= 64)  // all keys of the sequence are in this tile's first rows
+        // Two instances, as only the first key tile of a sequence has such queries: in one
+        // loop the test cost 4% of a dense walk.  (So did the same condition written
+        // with few_end.)
+        if (Lk <= 64 || (a.causal && j0 == 0 && off < 64))
             for (int t = 0; t < nt; ++t) tile(t, std::true_type{});
         else
             for (int t = 0; t < nt; ++t) tile(t, std::false_type{});
@@ -799,8 +819,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_ready);
             }
-            // (two instances: the test for a single tile inside the loop cost it 8%)
-            auto tile = [&](auto only) {
+            const bool few = left + 32 * kg < 64;  // all keys of this row are in the first tile
+            // (two instances: a test for the first tile inside the loop cost it 8%)
+            auto tile = [&](auto head) {
                 ok = wait_bar(&s_full[b], phase, abort_flag, a.status, a.limit) && ok;
                 tc_fence_after();
                 const uint32_t scol = tmem + lane_base + b * 64 + 32 * kg;
@@ -816,8 +837,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                         dp[e] = e <= left ? dp[e] : 0.f;
                     }
                 }
-                if constexpr (only.value) {
-                    // the only tile: delta is the sum of P dP over it
+                if constexpr (head.value) {
+                    // the first tile, where it holds all keys of some rows: their delta is the
+                    // sum of P dP over it
                     float sum = 0.f;
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -830,7 +852,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                     if (lane == 0) mbar_arrive(&pair[wq]);
                     // (bounded, as every wait; the next write is behind the next unit's q_ready)
                     ok = wait_bar(&pair[wq], singles++ & 1u, abort_flag, a.status, a.limit) && ok;
-                    sum += red[128 * (kg ^ 1) + r];
+                    sum = few ? sum + red[128 * (kg ^ 1) + r] : -nDr;
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
                         gk[e >> 1] = pack_bf16(sv[e] * (dp[e] - sum), sv[e + 1] * (dp[e + 1] - sum));
@@ -856,10 +878,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 left -= 64;
                 left0 -= 64;
             };
-            if (nt == 1)
+            int t = 0;
+            if (nt > 0 && left0 < 64) {
                 tile(std::true_type{});
-            else
-                for (int t = 0; t < nt; ++t) tile(std::false_type{});
+                t = 1;
+            }
+            for (; t < nt; ++t) tile(std::false_type{});
             // the next unit's rows travel while this one ends
             ok = __all_sync(0xffffffffu, ok);  // (lanes may have given up apart; the vote in `arrived` is the warp's)
             ok = ok && arrived(n + 1);
