@@ -2,7 +2,9 @@
 // one new token per sequence over it.
 //
 // append: a copy, bounded by HBM.  One thread a 16-byte piece of the rows; the
-// first threads of a CTA find the place of its tokens once for all of them.
+// first threads of a CTA find the place of its tokens once for all of them, and
+// every CTA looks at every border: if one does not ascend or leaves the rows given,
+// none writes anything.
 //
 // paged attention: every cached row is read once, 4 D bytes for 4 D flop and
 // query head, so HBM bounds it at any group size.  Work is cut into tiles of 64
@@ -110,13 +112,19 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
             place[1][threadIdx.x] = pv;
         }
     }
-    bad = __syncthreads_or(bad);
+    bool crooked = false;
+    if (a.cu != nullptr)
+        for (int s = threadIdx.x; s < a.c.seqs; s += 256)
+            crooked |= a.cu[s] < 0 || a.cu[s + 1] < a.cu[s] || a.cu[s + 1] > a.total;
+    crooked = __syncthreads_or(crooked);
+    bad = __syncthreads_or(bad || crooked);
     if (threadIdx.x == 0 && a.status != nullptr) {
         if (all)
             *a.status = bad ? kDevParam : kDevOk;
         else if (bad && !a.status_by_kernel)
             atomicExch(a.status, kDevParam);
     }
+    if (crooked) return;
     for (int base = threadIdx.x; base < n; base += U * 256) {
         if (base != threadIdx.x) fetch(base);
 #pragma unroll

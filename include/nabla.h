@@ -292,7 +292,8 @@ int nabla_attn_bwd(const nabla_shape *shape, const nabla_params *params, const n
  *     neighbouring batch entries, heads and tokens; the D features of a row are
  *     contiguous.  Distances of dimensions of size one are not looked at.
  *   - sequence borders, positions, lengths and page numbers are device memory
- *     and so unknown to the host; each call says what it does with bad ones.
+ *     and so unknown to the host; each call says what it does with bad ones.  A
+ *     call that has no rows to write does not look at them.
  * ------------------------------------------------------------------------- */
 typedef struct {
     void *data;
@@ -405,10 +406,11 @@ typedef struct {
 /* Writes rows k, v ([total, heads_kv, D] views) of packed sequences behind
  * their first starts[s] rows: token i of sequence s (cu[s] <= row < cu[s+1];
  * cu may be NULL for one token each, total = seqs) goes to row starts[s] + i.
- * A row that falls outside the table or on a page outside the pool is skipped
- * and, when a workspace (256 bytes) is given, reported as NABLA_ERR_PARAM in its
- * status; with workspace NULL it is skipped silently.  Two sequences must not
- * write the same page rows in one call.  D a multiple of 8, 16-byte views. */
+ * Borders that do not ascend, or that leave [0, total], make the call write
+ * nothing.  A row that falls outside the table or on a page outside the pool is
+ * skipped.  Either is reported, when a workspace (256 bytes) is given, as
+ * NABLA_ERR_PARAM in its status, and with workspace NULL goes unreported.  Rows of no
+ * sequence are skipped.  Two sequences must not write the same page rows in one call.  D a multiple of 8, 16-byte views. */
 int nabla_cache_append(const nabla_cache *cache, const nabla_view *k, const nabla_view *v,
                        int64_t total, const int32_t *starts, const int32_t *cu, void *workspace,
                        size_t workspace_bytes, nabla_stream_t stream);
