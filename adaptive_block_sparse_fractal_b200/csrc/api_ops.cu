@@ -9,6 +9,7 @@
 #include "packed.cuh"
 #include "paged.cuh"
 #include "rope.cuh"
+#include "views.h"
 
 // launchers (rope.cu, packed_fwd.cu, packed_bwd.cu, paged.cu)
 cudaError_t nabla_launch_rope(nabla::RopeArgs &a, int dtype, int layout, int wide,
@@ -22,7 +23,6 @@ cudaError_t nabla_launch_paged(const nabla::PagedArgs &a, cudaStream_t stream);
 namespace {
 
 constexpr size_t kStatusBytes = 256;
-constexpr int64_t kMaxExtent = 1ll << 46;  // bytes a view may span: keeps the arithmetic in 64 bits
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? NABLA_OK : NABLA_ERR_CUDA; }
@@ -36,78 +36,12 @@ int check_workspace(const void *ws, size_t bytes, size_t need) {
     return NABLA_OK;
 }
 
-// A view over [batch, heads, tokens, D] elements of `size` bytes.
-struct Box {
-    const nabla_view *v;
-    int64_t n[3], stride[3];  // batch, head, token: extents and distances (0 where the extent is 1)
-    int64_t D, size;
-    uintptr_t lo, hi;         // bytes it spans: [lo, hi)
-};
-
-// Extents and span; false for negative distances or a span beyond kMaxExtent.
-bool make_box(const nabla_view *v, int64_t B, int64_t heads, int64_t tokens, int64_t D, int size,
-              Box *b) {
-    b->v = v;
-    const int64_t n[3] = {B, heads, tokens}, s[3] = {v->batch, v->head, v->token};
-    int64_t last = D;
-    for (int i = 0; i < 3; ++i) {
-        b->n[i] = n[i];
-        b->stride[i] = n[i] > 1 ? s[i] : 0;
-        if (b->stride[i] < 0 || b->stride[i] > kMaxExtent) return false;
-        if (n[i] > 1 && b->stride[i] > kMaxExtent / n[i]) return false;
-        last += (n[i] - 1) * b->stride[i];
-    }
-    if (last > kMaxExtent / size) return false;
-    b->D = D;
-    b->size = size;
-    b->lo = reinterpret_cast<uintptr_t>(v->data);
-    b->hi = b->lo + static_cast<uintptr_t>(last) * size;
-    return true;
-}
-
-bool multiple_of_16(const Box &b) {
-    if ((b.lo & 15u) != 0) return false;
-    for (int i = 0; i < 3; ++i)
-        if (b.stride[i] * b.size % 16 != 0) return false;
-    return true;
-}
-
-// No two rows of a view that is written may share elements: walking its
-// dimensions from the closest together, each distance clears what lies inside.
-bool self_disjoint(const Box &b) {
-    bool used[3] = {b.n[0] == 1, b.n[1] == 1, b.n[2] == 1};
-    int64_t inner = b.D;
-    for (int round = 0; round < 3; ++round) {
-        int best = -1;
-        for (int i = 0; i < 3; ++i)
-            if (!used[i] && (best < 0 || b.stride[i] < b.stride[best])) best = i;
-        if (best < 0) break;
-        if (b.stride[best] < inner) return false;
-        inner += (b.n[best] - 1) * b.stride[best];
-        used[best] = true;
-    }
-    return true;
-}
-
-// Whether two views share no element: disjoint spans, or slices of one buffer
-// that repeat at the same token distance and lie beside each other in it.
-bool disjoint(const Box &a, const Box &b) {
-    if (a.hi <= b.lo || b.hi <= a.lo) return true;
-    const int64_t step = a.stride[2] * a.size;
-    if (step <= 0 || step != b.stride[2] * b.size) return false;
-    for (const Box *x : {&a, &b})
-        if (x->n[0] > 1 && x->stride[0] * x->size % step != 0) return false;
-    const int64_t wa = ((a.n[1] - 1) * a.stride[1] + a.D) * a.size;
-    const int64_t wb = ((b.n[1] - 1) * b.stride[1] + b.D) * b.size;
-    const int64_t d = b.lo >= a.lo ? static_cast<int64_t>((b.lo - a.lo) % step)
-                                   : (step - static_cast<int64_t>((a.lo - b.lo) % step)) % step;
-    return d >= wa && d + wb <= step;
-}
-
-bool same_view(const Box &a, const Box &b) {
-    return a.lo == b.lo && a.stride[0] == b.stride[0] && a.stride[1] == b.stride[1] &&
-           a.stride[2] == b.stride[2];
-}
+using nabla::views::Box;
+using nabla::views::disjoint;
+using nabla::views::make_box;
+using nabla::views::multiple_of_16;
+using nabla::views::same_view;
+using nabla::views::self_disjoint;
 
 // ---------------------------------------------------------------------------
 // packed attention
@@ -171,7 +105,7 @@ nabla::packed::View dev_view(const nabla_view *v) {
 
 int packed_view(const nabla_view *v, int64_t tokens, int heads, int D, bool written, Box *b) {
     if (v == nullptr) return NABLA_ERR_NULL;
-    if (tokens == 0) return make_box(v, 1, 1, 1, D, 2, b) ? NABLA_OK : NABLA_ERR_PARAM;
+    if (tokens == 0) return make_box(v, 1, heads, 0, D, 2, b) ? NABLA_OK : NABLA_ERR_PARAM;  // (empty)
     if (v->data == nullptr) return NABLA_ERR_NULL;
     if (!make_box(v, 1, heads, tokens, D, 2, b)) return NABLA_ERR_PARAM;
     if (!multiple_of_16(*b)) return NABLA_ERR_ALIGN;
@@ -377,9 +311,7 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
         (st = packed_view(o, shape->total_q, shape->heads, shape->D, true, &bo)) != NABLA_OK)
         return st;
     if (!aligned4(lse)) return NABLA_ERR_ALIGN;
-    if (shape->total_q > 0 && (!disjoint(bo, bq) || (shape->total_k > 0 &&
-                                                     (!disjoint(bo, bk) || !disjoint(bo, bv)))))
-        return NABLA_ERR_PARAM;
+    if (!disjoint(bo, bq) || !disjoint(bo, bk) || !disjoint(bo, bv)) return NABLA_ERR_PARAM;
     const int64_t units = fwd_units(shape);
     const int splits = fwd_splits(shape);
     if (units > INT32_MAX / splits) return NABLA_ERR_SHAPE;
@@ -423,13 +355,10 @@ int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const 
     if (!aligned4(lse)) return NABLA_ERR_ALIGN;
     // the three kernels read the inputs while the first outputs are written
     for (int i = 0; i < 3; ++i) {
-        if ((out_q[i] ? shape->total_q : shape->total_k) == 0) continue;
-        for (int j = 0; j < 5; ++j)
-            if ((of_q[j] ? shape->total_q : shape->total_k) > 0 && !disjoint(bo[i], bi[j]))
-                return NABLA_ERR_PARAM;
+        for (const Box &x : bi)
+            if (!disjoint(bo[i], x)) return NABLA_ERR_PARAM;
         for (int j = 0; j < i; ++j)
-            if ((out_q[j] ? shape->total_q : shape->total_k) > 0 && !disjoint(bo[i], bo[j]))
-                return NABLA_ERR_PARAM;
+            if (!disjoint(bo[i], bo[j])) return NABLA_ERR_PARAM;
     }
     const int64_t G = shape->heads / shape->heads_kv;
     const int64_t q_tiles = shape->total_q / 64 + shape->seqs;
