@@ -411,12 +411,11 @@ int nabla_cache_append(const nabla_cache *cache, const nabla_view *k, const nabl
             !make_box(v, 1, cache->heads_kv, total, cache->D, 2, &bv))
             return NABLA_ERR_PARAM;
         if (!multiple_of_16(bk) || !multiple_of_16(bv)) return NABLA_ERR_ALIGN;
-        // rows that lie in the pool itself could be overwritten before they are read;
-        // K and V of one pool are views of one buffer, so only their rows may not coincide
+        // K and V may be slices of one buffer, but share no row; rows that lie in a pool
+        // could be overwritten before they are read
+        if (!disjoint(pool[0], pool[1])) return NABLA_ERR_PARAM;
         for (const Box &p : pool)
-            if (!(bk.hi <= p.lo || p.hi <= bk.lo) || !(bv.hi <= p.lo || p.hi <= bv.lo))
-                return NABLA_ERR_PARAM;
-        if (same_view(pool[0], pool[1])) return NABLA_ERR_PARAM;
+            if (!disjoint(bk, p) || !disjoint(bv, p)) return NABLA_ERR_PARAM;
     }
     cudaStream_t s = as_stream(stream);
     // a few rows: one CTA of the launch looks at all of them and writes the status

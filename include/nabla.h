@@ -410,7 +410,9 @@ typedef struct {
  * nothing.  A row that falls outside the table or on a page outside the pool is
  * skipped.  Either is reported, when a workspace (256 bytes) is given, as
  * NABLA_ERR_PARAM in its status, and with workspace NULL goes unreported.  Rows of no
- * sequence are skipped.  Two sequences must not write the same page rows in one call.  D a multiple of 8, 16-byte views. */
+ * sequence are skipped.  Two sequences must not write the same page rows in one call.
+ * The k and v pools may be slices of one buffer; rows that they share, with each
+ * other or with the rows given, are NABLA_ERR_PARAM.  D a multiple of 8, 16-byte views. */
 int nabla_cache_append(const nabla_cache *cache, const nabla_view *k, const nabla_view *v,
                        int64_t total, const int32_t *starts, const int32_t *cu, void *workspace,
                        size_t workspace_bytes, nabla_stream_t stream);
