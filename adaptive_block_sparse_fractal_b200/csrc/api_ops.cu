@@ -4,6 +4,7 @@
 // error is returned before anything is enqueued.
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/nabla.h"
 #include "packed.cuh"
@@ -38,10 +39,24 @@ int check_workspace(const void *ws, size_t bytes, size_t need) {
 
 using nabla::views::Box;
 using nabla::views::disjoint;
+using nabla::views::flat;
 using nabla::views::make_box;
 using nabla::views::multiple_of_16;
 using nabla::views::same_view;
 using nabla::views::self_disjoint;
+
+// Whether no output shares a byte with an input or with another output.
+bool apart(std::initializer_list<Box> outs, std::initializer_list<Box> ins) {
+    for (const Box *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Box &i : ins)
+            if (!disjoint(*o, i)) return false;
+        for (const Box *p = outs.begin(); p != o; ++p)
+            if (!disjoint(*o, *p)) return false;
+    }
+    return true;
+}
+
+Box ints(const int32_t *p, int64_t n) { return flat(p, 4 * n); }
 
 // ---------------------------------------------------------------------------
 // packed attention
@@ -255,6 +270,9 @@ int nabla_rope(const nabla_rope_params *p, int B, int T, int H, int W, int P, in
     // in place: each thread writes exactly the elements it has read, if both
     // sides have the same order (both flattened counts as the same)
     const bool same_order = ((p->flags & NABLA_ROPE_FLAT_IN) != 0) == ((p->flags & NABLA_ROPE_FLAT_OUT) != 0);
+    const Box places = ints(pos, (pos_batch > 0 ? (B - 1) * pos_batch : 0) + N * pos_axes);
+    for (int i = 0; i < n; ++i)
+        if (!disjoint(bo[i], places)) return NABLA_ERR_PARAM;
     for (int i = 0; i < n; ++i)
         for (int j = 0; j < n; ++j) {
             if (!(i == j && same_order && same_view(bo[i], bi[i])) && !disjoint(bo[i], bi[j]))
@@ -311,7 +329,10 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
         (st = packed_view(o, shape->total_q, shape->heads, shape->D, true, &bo)) != NABLA_OK)
         return st;
     if (!aligned4(lse)) return NABLA_ERR_ALIGN;
-    if (!disjoint(bo, bq) || !disjoint(bo, bk) || !disjoint(bo, bv)) return NABLA_ERR_PARAM;
+    const int64_t lse_bytes = 4 * shape->total_q * shape->heads, borders = shape->seqs + 1;
+    if (!apart({bo, flat(lse, lse_bytes), flat(workspace, packed_ws(shape, NABLA_PACKED_FWD))},
+               {bq, bk, bv, ints(cu_q, borders), ints(cu_k, borders)}))
+        return NABLA_ERR_PARAM;
     const int64_t units = fwd_units(shape);
     const int splits = fwd_splits(shape);
     if (units > INT32_MAX / splits) return NABLA_ERR_SHAPE;
@@ -354,12 +375,10 @@ int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const 
     if (shape->total_q > 0 && lse == nullptr) return NABLA_ERR_NULL;
     if (!aligned4(lse)) return NABLA_ERR_ALIGN;
     // the three kernels read the inputs while the first outputs are written
-    for (int i = 0; i < 3; ++i) {
-        for (const Box &x : bi)
-            if (!disjoint(bo[i], x)) return NABLA_ERR_PARAM;
-        for (int j = 0; j < i; ++j)
-            if (!disjoint(bo[i], bo[j])) return NABLA_ERR_PARAM;
-    }
+    const int64_t lse_bytes = 4 * shape->total_q * shape->heads, borders = shape->seqs + 1;
+    if (!apart({bo[0], bo[1], bo[2], flat(workspace, packed_ws(shape, NABLA_PACKED_BWD))},
+               {bi[0], bi[1], bi[2], bi[3], bi[4], flat(lse, lse_bytes), ints(cu_q, borders), ints(cu_k, borders)}))
+        return NABLA_ERR_PARAM;
     const int64_t G = shape->heads / shape->heads_kv;
     const int64_t q_tiles = shape->total_q / 64 + shape->seqs;
     const int64_t row_tiles = shape->total_q * G / 128 + shape->seqs;
@@ -413,9 +432,10 @@ int nabla_cache_append(const nabla_cache *cache, const nabla_view *k, const nabl
         if (!multiple_of_16(bk) || !multiple_of_16(bv)) return NABLA_ERR_ALIGN;
         // K and V may be slices of one buffer, but share no row; rows that lie in a pool
         // could be overwritten before they are read
-        if (!disjoint(pool[0], pool[1])) return NABLA_ERR_PARAM;
-        for (const Box &p : pool)
-            if (!disjoint(bk, p) || !disjoint(bv, p)) return NABLA_ERR_PARAM;
+        if (!apart({pool[0], pool[1], flat(workspace, kStatusBytes)},
+                   {bk, bv, ints(starts, cache->seqs), ints(cu, cache->seqs + 1ll),
+                    ints(cache->table, static_cast<int64_t>(cache->seqs) * cache->table_width)}))
+            return NABLA_ERR_PARAM;
     }
     cudaStream_t s = as_stream(stream);
     // a few rows: one CTA of the launch looks at all of them and writes the status
@@ -465,7 +485,10 @@ int nabla_attn_paged(const nabla_cache *cache, int heads, float scale, const nab
         !make_box(o, 1, heads, cache->seqs, cache->D, 2, &bo))
         return NABLA_ERR_PARAM;
     if (!multiple_of_16(bq) || !multiple_of_16(bo)) return NABLA_ERR_ALIGN;
-    if (!self_disjoint(bo) || !disjoint(bo, bq) || !disjoint(bo, pool[0]) || !disjoint(bo, pool[1]))
+    if (!self_disjoint(bo) ||
+        !apart({bo, flat(lse, 4ll * cache->seqs * heads), flat(workspace, paged_ws(cache))},
+               {bq, pool[0], pool[1], ints(lens, cache->seqs),
+                ints(cache->table, static_cast<int64_t>(cache->seqs) * cache->table_width)}))
         return NABLA_ERR_PARAM;
     a.q = static_cast<const __nv_bfloat16 *>(q->data);
     a.o = static_cast<__nv_bfloat16 *>(o->data);

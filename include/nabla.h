@@ -291,6 +291,8 @@ int nabla_attn_bwd(const nabla_shape *shape, const nabla_params *params, const n
  *   - tensors are views: a base pointer and the distances in ELEMENTS between
  *     neighbouring batch entries, heads and tokens; the D features of a row are
  *     contiguous.  Distances of dimensions of size one are not looked at.
+ *   - no output, the lse and the workspace among them, may overlap an input or
+ *     another output (NABLA_ERR_PARAM), but for what a call says of itself.
  *   - sequence borders, positions, lengths and page numbers are device memory
  *     and so unknown to the host; each call says what it does with bad ones.  A
  *     call that has no rows to write does not look at them.
