@@ -38,9 +38,11 @@ inline cudaError_t nabla_launch_early(void (*kernel)(P...), unsigned grid, unsig
 }
 
 // Host: dynamic shared memory of a kernel on the current device.  The attribute
-// holds for the process; only the first call on a device sets it.
+// holds for the process; only the first call on a device sets it.  (Internal linkage:
+// as an inline function its `set` would be one object for all copies of this library
+// in a process, whose kernels each need the attribute.)
 template <auto kKernel>
-inline cudaError_t nabla_allow_smem(uint32_t bytes) {
+static cudaError_t nabla_allow_smem(uint32_t bytes) {
     static std::atomic<uint64_t> set{0};  // one bit a device
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
