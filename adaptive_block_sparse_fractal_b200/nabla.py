@@ -148,7 +148,7 @@ def _check(status, what):
 
 def _stream(t):
     """The current stream of the tensor's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return torch._C._cuda_getCurrentRawStream(_device(t, "the workspace"))
 
 
 def _ptr(t):
