@@ -294,6 +294,9 @@ int nabla_rope(const nabla_rope_params *p, int B, int T, int H, int W, int P, in
     a.pos_batch = pos_batch;
     a.pos_axes = pos_axes;
     constexpr double kTwoPi = 6.283185307179586476925286766559;
+    // largest distance from 0 of a position on each axis
+    const double reach[3] = {pos != nullptr ? 2147483648.0 : T, pos != nullptr ? 2147483648.0 : H,
+                             pos != nullptr ? 2147483648.0 : W};
     for (int ax = 0, at = 0; ax < 3; ++ax) {
         a.offset[ax] = p->pairs[ax] > 0 ? p->offset[ax] : 0.0;
         // theta^(-i / n): a power for every eighth pair, products of up to 7 ratios
@@ -304,6 +307,9 @@ int nabla_rope(const nabla_rope_params *p, int B, int T, int H, int W, int P, in
             f = i % 8 == 0 ? std::pow(p->theta[ax], -static_cast<double>(i) / p->pairs[ax]) : f * ratio;
             a.axis[at] = static_cast<int8_t>(ax);
             a.turn[at] = ((p->flags & NABLA_ROPE_INVERSE) ? -1.0 : 1.0) * p->scale[ax] * f / kTwoPi;
+            // the reduction to an eighth of a turn holds below 2^49 turns (float64 knows no
+            // more of the angle there); this refuses infinities and NaN as well
+            if (!((reach[ax] + std::fabs(a.offset[ax])) * std::fabs(a.turn[at]) < 0x1p49)) return NABLA_ERR_PARAM;
         }
     }
     return cuda_status(nabla_launch_rope(a, p->dtype, p->layout, wide, as_stream(stream)));

@@ -321,7 +321,9 @@ typedef struct {
  *           behind the rotated ones are copied.  0 leaves an axis out.
  *   theta, scale, offset   the pair i of axis a turns by
  *           (position_a + offset[a]) * scale[a] * theta[a]^(-i / pairs[a]),
- *           taken in float64 before its sine and cosine. */
+ *           taken in float64 before its sine and cosine.  Values that would turn
+ *           the farthest position (with `pos`: 2^31) by 2^49 turns or more are
+ *           NABLA_ERR_PARAM. */
 typedef struct {
     int dtype, layout, D;
     int pairs[3];
