@@ -29,6 +29,9 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? NABLA_OK : NABLA_ERR_CUDA; }
 cudaStream_t as_stream(nabla_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
+// (the kernels take scale * log2(e))
+bool scale_ok(float s) { return s > 0.f && std::isfinite(s * 1.4426950408889634f); }
+
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int check_workspace(const void *ws, size_t bytes, size_t need) {
@@ -136,7 +139,7 @@ int check_packed(const nabla_packed *s, const int32_t *cu_q, const int32_t *cu_k
                  size_t bytes) {
     if (s == nullptr) return NABLA_ERR_NULL;
     if (!packed_shape_ok(s)) return NABLA_ERR_SHAPE;
-    if (!(s->scale > 0.f) || !std::isfinite(s->scale) ||
+    if (!scale_ok(s->scale) ||
         (s->causal & ~static_cast<int>(1u | NABLA_DEBUG_TIMEOUT)) != 0)
         return NABLA_ERR_PARAM;
     if (cu_q == nullptr || cu_k == nullptr) return NABLA_ERR_NULL;
@@ -476,7 +479,7 @@ int nabla_attn_paged(const nabla_cache *cache, int heads, float scale, const nab
     if (cache == nullptr || q == nullptr || o == nullptr) return NABLA_ERR_NULL;
     if (nabla_paged_workspace_size(cache, heads) == 0) return NABLA_ERR_SHAPE;
     if (static_cast<int64_t>(cache->seqs) * heads > INT32_MAX) return NABLA_ERR_SHAPE;
-    if (!(scale > 0.f) || !std::isfinite(scale)) return NABLA_ERR_PARAM;
+    if (!scale_ok(scale)) return NABLA_ERR_PARAM;
     int st = check_workspace(workspace, workspace_bytes, paged_ws(cache));
     if (st != NABLA_OK) return st;
     cudaStream_t s = as_stream(stream);
