@@ -958,8 +958,13 @@ static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_til
         constexpr uint32_t kSmem = KvLayout<D>::kSmem;
         err = nabla_allow_smem<dkdv_kernel<D>>(kSmem);
         if (err != cudaSuccess) return err;
-        err = nabla_launch_early(dkdv_kernel<D>, static_cast<unsigned>(key_tiles * a.heads_kv), kKvThreads, kSmem,
-                                 stream, mq, mv128, mdo, a);
+        const unsigned grid = static_cast<unsigned>(key_tiles * a.heads_kv);
+        if (q) {
+            err = nabla_launch_early(dkdv_kernel<D>, grid, kKvThreads, kSmem, stream, mq, mv128, mdo, a);
+        } else {  // without pre_kernel its predecessor is what clears the status, which it reads at once
+            dkdv_kernel<D><<<grid, kKvThreads, kSmem, stream>>>(mq, mv128, mdo, a);
+            err = cudaGetLastError();
+        }
         if (err != cudaSuccess) return err;
     }
     if (q) {
