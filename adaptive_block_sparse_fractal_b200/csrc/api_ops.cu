@@ -49,12 +49,12 @@ using nabla::views::same_view;
 using nabla::views::self_disjoint;
 
 // Whether no output shares a byte with an input or with another output.
-bool apart(std::initializer_list<Box> outs, std::initializer_list<Box> ins) {
-    for (const Box *o = outs.begin(); o != outs.end(); ++o) {
-        for (const Box &i : ins)
-            if (!disjoint(*o, i)) return false;
-        for (const Box *p = outs.begin(); p != o; ++p)
-            if (!disjoint(*o, *p)) return false;
+bool apart(std::initializer_list<const Box *> outs, std::initializer_list<const Box *> ins) {
+    for (const Box *const *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Box *i : ins)
+            if (!disjoint(**o, *i)) return false;
+        for (const Box *const *p = outs.begin(); p != o; ++p)
+            if (!disjoint(**o, **p)) return false;
     }
     return true;
 }
@@ -338,10 +338,9 @@ int nabla_attn_packed_fwd(const nabla_packed *shape, const nabla_view *q, const 
         (st = packed_view(o, shape->total_q, shape->heads, shape->D, true, &bo)) != NABLA_OK)
         return st;
     if (!aligned4(lse)) return NABLA_ERR_ALIGN;
-    const int64_t lse_bytes = 4 * shape->total_q * shape->heads, borders = shape->seqs + 1;
-    if (!apart({bo, flat(lse, lse_bytes), flat(workspace, packed_ws(shape, NABLA_PACKED_FWD))},
-               {bq, bk, bv, ints(cu_q, borders), ints(cu_k, borders)}))
-        return NABLA_ERR_PARAM;
+    const Box bl = flat(lse, 4 * shape->total_q * shape->heads), bw = flat(workspace, packed_ws(shape, NABLA_PACKED_FWD)),
+              cq = ints(cu_q, shape->seqs + 1), ck = ints(cu_k, shape->seqs + 1);
+    if (!apart({&bo, &bl, &bw}, {&bq, &bk, &bv, &cq, &ck})) return NABLA_ERR_PARAM;
     const int64_t units = fwd_units(shape);
     const int splits = fwd_splits(shape);
     if (units > INT32_MAX / splits) return NABLA_ERR_SHAPE;
@@ -384,9 +383,9 @@ int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const 
     if (shape->total_q > 0 && lse == nullptr) return NABLA_ERR_NULL;
     if (!aligned4(lse)) return NABLA_ERR_ALIGN;
     // the three kernels read the inputs while the first outputs are written
-    const int64_t lse_bytes = 4 * shape->total_q * shape->heads, borders = shape->seqs + 1;
-    if (!apart({bo[0], bo[1], bo[2], flat(workspace, packed_ws(shape, NABLA_PACKED_BWD))},
-               {bi[0], bi[1], bi[2], bi[3], bi[4], flat(lse, lse_bytes), ints(cu_q, borders), ints(cu_k, borders)}))
+    const Box bl = flat(lse, 4 * shape->total_q * shape->heads), bw = flat(workspace, packed_ws(shape, NABLA_PACKED_BWD)),
+              cq = ints(cu_q, shape->seqs + 1), ck = ints(cu_k, shape->seqs + 1);
+    if (!apart({&bo[0], &bo[1], &bo[2], &bw}, {&bi[0], &bi[1], &bi[2], &bi[3], &bi[4], &bl, &cq, &ck}))
         return NABLA_ERR_PARAM;
     const int64_t G = shape->heads / shape->heads_kv;
     const int64_t q_tiles = shape->total_q / 64 + shape->seqs;
@@ -441,10 +440,9 @@ int nabla_cache_append(const nabla_cache *cache, const nabla_view *k, const nabl
         if (!multiple_of_16(bk) || !multiple_of_16(bv)) return NABLA_ERR_ALIGN;
         // K and V may be slices of one buffer, but share no row; rows that lie in a pool
         // could be overwritten before they are read
-        if (!apart({pool[0], pool[1], flat(workspace, kStatusBytes)},
-                   {bk, bv, ints(starts, cache->seqs), ints(cu, cache->seqs + 1ll),
-                    ints(cache->table, static_cast<int64_t>(cache->seqs) * cache->table_width)}))
-            return NABLA_ERR_PARAM;
+        const Box bw = flat(workspace, kStatusBytes), bs = ints(starts, cache->seqs), bc = ints(cu, cache->seqs + 1ll),
+                  bt = ints(cache->table, static_cast<int64_t>(cache->seqs) * cache->table_width);
+        if (!apart({&pool[0], &pool[1], &bw}, {&bk, &bv, &bs, &bc, &bt})) return NABLA_ERR_PARAM;
     }
     cudaStream_t s = as_stream(stream);
     // a few rows: one CTA of the launch looks at all of them and writes the status
@@ -494,11 +492,9 @@ int nabla_attn_paged(const nabla_cache *cache, int heads, float scale, const nab
         !make_box(o, 1, heads, cache->seqs, cache->D, 2, &bo))
         return NABLA_ERR_PARAM;
     if (!multiple_of_16(bq) || !multiple_of_16(bo)) return NABLA_ERR_ALIGN;
-    if (!self_disjoint(bo) ||
-        !apart({bo, flat(lse, 4ll * cache->seqs * heads), flat(workspace, paged_ws(cache))},
-               {bq, pool[0], pool[1], ints(lens, cache->seqs),
-                ints(cache->table, static_cast<int64_t>(cache->seqs) * cache->table_width)}))
-        return NABLA_ERR_PARAM;
+    const Box bl = flat(lse, 4ll * cache->seqs * heads), bw = flat(workspace, paged_ws(cache)), bn = ints(lens, cache->seqs),
+              bt = ints(cache->table, static_cast<int64_t>(cache->seqs) * cache->table_width);
+    if (!self_disjoint(bo) || !apart({&bo, &bl, &bw}, {&bq, &pool[0], &pool[1], &bn, &bt})) return NABLA_ERR_PARAM;
     a.q = static_cast<const __nv_bfloat16 *>(q->data);
     a.o = static_cast<__nv_bfloat16 *>(o->data);
     a.q_head = bq.stride[1];

@@ -99,9 +99,8 @@ inline int add_terms(const Box &b, int sign, Term *t, int n) {
 
 inline bool by_step(const Term &a, const Term &b) { return a.step > b.step; }
 
-// Whether two views share no byte.
-inline bool disjoint(const Box &a, const Box &b) {
-    if (a.lo == a.hi || b.lo == b.hi || a.hi <= b.lo || b.hi <= a.lo) return true;
+// Whether two views share no byte, where the bytes that they span do.
+inline bool rows_apart(const Box &a, const Box &b) {
     Term t[6];
     const int n = add_terms(b, -1, t, add_terms(a, 1, t, 0));
     std::sort(t, t + n, by_step);
@@ -109,6 +108,10 @@ inline bool disjoint(const Box &a, const Box &b) {
     const int64_t first = a.lo >= b.lo ? static_cast<int64_t>(a.lo - b.lo) : -static_cast<int64_t>(b.lo - a.lo);
     int work = kSearch;
     return !reaches(t, n, 1 - a.row - first, b.row - 1 - first, &work);
+}
+// Whether two views share no byte.
+inline bool disjoint(const Box &a, const Box &b) {
+    return a.lo == a.hi || b.lo == b.hi || a.hi <= b.lo || b.hi <= a.lo || rows_apart(a, b);
 }
 
 // Whether no two rows of a view share a byte (one that is written must not).
@@ -121,9 +124,14 @@ inline bool self_disjoint(const Box &b) {
         t[n++] = {b.step[i], 1 - b.n[i], b.n[i] - 1};
     }
     std::sort(t, t + n, by_step);
+    // commonly each step clears what lies inside it
+    int64_t inner = b.row;
+    int i = n - 1;
+    for (; i >= 0 && t[i].step >= inner; --i) inner += t[i].hi * t[i].step;
+    if (i < 0) return true;
     // two rows differ first in dimension i, there by a positive number of steps
     int work = kSearch;
-    for (int i = 0; i < n; ++i) {
+    for (i = 0; i < n; ++i) {
         Term d[3];
         std::copy(t + i, t + n, d);
         d[0].lo = 1;
