@@ -394,8 +394,8 @@ int nabla_attn_packed_bwd(const nabla_packed *shape, const nabla_view *q, const 
     if (row_tiles * shape->heads_kv > INT32_MAX || key_tiles * shape->heads_kv > INT32_MAX)
         return NABLA_ERR_SHAPE;
     cudaStream_t s = as_stream(stream);
-    // the status word and the unit counter behind it
-    if (cudaMemsetAsync(workspace, 0, 2 * sizeof(int), s) != cudaSuccess) return NABLA_ERR_CUDA;
+    // the status word, the unit counter and the verdict on the borders behind it
+    if (cudaMemsetAsync(workspace, 0, 3 * sizeof(int), s) != cudaSuccess) return NABLA_ERR_CUDA;
     if (shape->total_q == 0 && shape->total_k == 0) return NABLA_OK;
     nabla::packed::Args a = packed_args(shape, cu_q, cu_k, workspace);
     a.q = dev_view(q);

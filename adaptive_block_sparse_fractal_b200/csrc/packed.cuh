@@ -21,7 +21,7 @@ struct Args {
     View q, k, v, o, dout, dq, dk, dv;
     const int32_t *cu_q, *cu_k;
     float *lse;        // [heads, total_q]
-    int *status;       // workspace status word; behind it the unit counter
+    int *status;       // workspace status word; behind it the unit counter and, in the backward, whether borders are bad
     float *pad_l, *pad_d;  // backward: [heads, pad_rows], -lse log2(e) and -dout.o
     float *part;       // split forward: partial rows, then their (m, l)
     int64_t total_q, total_k, pad_rows;
@@ -36,75 +36,54 @@ struct Args {
 struct SeqTile {
     int seq, tile;      // tile within the sequence
     int q0, Lq, k0, Lk;
-    int pad;            // 64-row tiles of the sequences in front
+    int pad;            // tile_slot of its 64-row tiles of q
 };
 
-// Finds the sequence that holds tile `unit`, sequences having `count(Lq, Lk)`
-// tiles each, by a scan of all threads of the CTA (NT of them) over the
-// borders.  Every CTA looks at every border: one that does not ascend or
-// leaves the tensors makes all of them give up before any output is written.
-// Returns false when the CTA has nothing to do.
-template <int NT, typename Count>
-__device__ __forceinline__ bool find_seq(const Args &a, int64_t unit, Count count, SeqTile *out,
-                                         int64_t *warp_sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kWarps = NT / 32;
-    int64_t carry = 0;  // low half: tiles, high half: 64-row tiles of q
-    if (threadIdx.x == 0) out->seq = -1;
-    bool bad = false;
-    for (int base = 0; base < a.seqs; base += NT) {
-        const int s = base + threadIdx.x;
-        int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-        if (s < a.seqs) {
-            q0 = a.cu_q[s];
-            q1 = a.cu_q[s + 1];
-            k0 = a.cu_k[s];
-            k1 = a.cu_k[s + 1];
-        }
-        bad |= q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k;
-        const int64_t n = bad ? 0 : count(q1 - q0, k1 - k0);
-        const int64_t mine = n | (static_cast<int64_t>(bad ? 0 : (q1 - q0 + 63) >> 6) << 32);
-        int64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
-        }
-        __syncthreads();  // the sums of the round before have been read
-        if (lane == 31) warp_sums[warp] = incl;
-        __syncthreads();
-        int64_t front = carry, all = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) front += warp_sums[w];
-            all += warp_sums[w];
-        }
-        carry += all;
-        const int64_t excl = front + incl - mine;
-        const int64_t before = excl & 0xffffffffll;
-        if (unit >= before && unit < before + n) {
-            out->seq = s;
-            out->tile = static_cast<int>(unit - before);
-            out->q0 = q0;
-            out->Lq = q1 - q0;
-            out->k0 = k0;
-            out->Lk = k1 - k0;
-            out->pad = static_cast<int>(excl >> 32);
-        }
+// Tiles of `len` rows are numbered so that those of sequence s begin at tile_slot(its
+// first border, len, s): each sequence has room for the tiles that it may need, as
+// floor((c + n) / len) + 1 >= floor(c / len) + ceil(n / len), there are total / len +
+// seqs of them at most, and no sum over the sequences in front is needed.
+__device__ __forceinline__ int tile_slot(int border, int len, int s) { return border / len + s; }
+
+// Finds the sequence that holds tile `unit` of `len` rows, of q or of k: every warp
+// searches by itself, 32 borders at a time (with a scan over all of them the work grew with
+// the square of the sequences: 20,000 of 20 rows took 27 ms backward, against 5.3).
+// Returns false when the CTA has nothing to do, be it that the borders around it are no
+// borders.  For the whole CTA.
+__device__ __forceinline__ bool find_seq(const Args &a, bool of_q, int len, int unit, SeqTile *out) {
+    const int lane = threadIdx.x & 31;
+    const int32_t *cu = of_q ? a.cu_q : a.cu_k;
+    int s = 0;
+    for (int n = a.seqs; n > 1;) {  // the last one of [s, s + n) that begins at or before `unit`
+        const int step = (n + 31) / 32, at = lane * step;
+        const uint32_t ok = __ballot_sync(0xffffffffu, at < n && tile_slot(cu[s + (at < n ? at : 0)], len, s + at) <= unit);
+        const int front = ok == 0 ? 0 : (31 - __clz(ok)) * step;
+        s += front;
+        n = min(step, n - front);
     }
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) atomicExch(a.status, kDevParam);
-        return false;
+    const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
+    const bool good = q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k;
+    const int tile = good ? unit - tile_slot(of_q ? q0 : k0, len, s) : -1;
+    if (threadIdx.x == 0) {
+        out->seq = tile >= 0 && tile < ((of_q ? q1 - q0 : k1 - k0) + len - 1) / len ? s : -1;
+        out->tile = tile;
+        out->q0 = q0;
+        out->Lq = q1 - q0;
+        out->k0 = k0;
+        out->Lk = k1 - k0;
+        out->pad = tile_slot(q0, 64, s);
     }
+    __syncthreads();
     return out->seq >= 0;
 }
 
 constexpr int kSms = 148;  // CTAs of a persistent launch
 
-// Every thread of the CTA looks at some borders; see find_seq.
-__device__ __forceinline__ bool borders_ok(const Args &a) {
+// Borders that do not ascend or leave the tensors make a call give up before any output
+// is written.  Every thread looks at some, `first` of `count` threads.
+__device__ __forceinline__ bool borders_ok(const Args &a, int64_t first, int count) {
     bool good = true;
-    for (int s = threadIdx.x; s < a.seqs; s += blockDim.x) {
+    for (int64_t s = first; s < a.seqs; s += count) {
         const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
         good = good && q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k;
     }
@@ -124,9 +103,7 @@ __device__ __forceinline__ uint32_t take_unit(const Args &a) {  // (units stay b
 struct UnitScan {
     int base, q0, q1, k0, k1;
     uint32_t front, all;     // tiles in front of this lane's sequence and of the next 32
-    int pad_front, pad_all;  // the same of 64-row tiles of q
-    __device__ __forceinline__ UnitScan()
-        : base(-32), q0(0), q1(0), k0(0), k1(0), front(0), all(0), pad_front(0), pad_all(0) {}
+    __device__ __forceinline__ UnitScan() : base(-32), q0(0), q1(0), k0(0), k1(0), front(0), all(0) {}
     // sequence and tile of unit x; false behind the last
     __device__ __forceinline__ bool find(const Args &a, uint32_t x, int mul, int len, int lane, SeqTile *u) {
         while (x >= all) {
@@ -144,22 +121,14 @@ struct UnitScan {
                 k1 = a.cu_k[s + 1];
             }
             const uint32_t mine = (static_cast<uint32_t>(q1 - q0) * mul + len - 1) / len;
-            const int pads = (q1 - q0 + 63) >> 6;
             uint32_t incl = mine;
-            int pincl = pads;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-                const int p = __shfl_up_sync(0xffffffffu, pincl, o);
-                if (lane >= o) {
-                    incl += t;
-                    pincl += p;
-                }
+                if (lane >= o) incl += t;
             }
             front = all + incl - mine;
-            pad_front = pad_all + pincl - pads;
             all += __shfl_sync(0xffffffffu, incl, 31);
-            pad_all += __shfl_sync(0xffffffffu, pincl, 31);
         }
         // the last lane whose sequence starts at or before x (empty ones share a start)
         const uint32_t at = __ballot_sync(0xffffffffu, front <= x);
@@ -169,7 +138,7 @@ struct UnitScan {
         u->Lq = __shfl_sync(0xffffffffu, q1, src) - u->q0;
         u->k0 = __shfl_sync(0xffffffffu, k0, src);
         u->Lk = __shfl_sync(0xffffffffu, k1, src) - u->k0;
-        u->pad = __shfl_sync(0xffffffffu, pad_front, src);
+        u->pad = tile_slot(u->q0, 64, u->seq);
         u->tile = static_cast<int>(x - __shfl_sync(0xffffffffu, front, src));
         return true;
     }

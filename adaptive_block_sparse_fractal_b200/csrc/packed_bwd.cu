@@ -50,10 +50,13 @@ constexpr int kPreThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kPreThreads) pre_kernel(const __grid_constant__ Args a, int per) {
     __shared__ SeqTile st;
-    __shared__ int64_t sums[kPreThreads / 32];
     allow_dependents();
-    if (!find_seq<kPreThreads>(a, blockIdx.x, [](int Lq, int) { return (Lq + 63) >> 6; }, &st, sums))
-        return;
+    // the borders, shared out over the launch (there are no fewer CTAs in x than sequences)
+    if (blockIdx.y == 0 && !borders_ok(a, static_cast<int64_t>(blockIdx.x) * kPreThreads + threadIdx.x, 1 << 30)) {
+        atomicExch(a.status, kDevParam);
+        atomicExch(a.status + 2, 1);
+    }
+    if (!find_seq(a, true, 64, blockIdx.x, &st)) return;
     constexpr int TPR = D / 8;  // threads per row, 8 features each
     constexpr int kStep = kPreThreads / TPR;
     const int sub = threadIdx.x % TPR;
@@ -104,8 +107,7 @@ struct KvLayout {
     static constexpr int kBars = 1 + 2 * kStages + 2 + 2 + 1 + 1 + 1 + 1;
     static constexpr uint32_t KV_COL = (KV_BAR + 8 * kBars + 15) / 16 * 16;  // sums over keys: [2][2][64]
     static constexpr uint32_t KV_SEQ = KV_COL + 2 * 2 * 64 * 4;
-    static constexpr uint32_t KV_SUM = (KV_SEQ + sizeof(SeqTile) + 7) / 8 * 8;
-    static constexpr uint32_t KV_INT = KV_SUM + 8 * (kKvThreads / 32);
+    static constexpr uint32_t KV_INT = (KV_SEQ + sizeof(SeqTile) + 7) / 8 * 8;
     static constexpr uint32_t kSmem = KV_INT + 16 + 1024;
 };
 
@@ -139,8 +141,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     volatile int *abort_flag = sInt + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hk = static_cast<int>(blockIdx.x % a.heads_kv);
-    if (!find_seq<kKvThreads>(a, blockIdx.x / a.heads_kv, [](int, int Lk) { return (Lk + 127) >> 7; }, st,
-                              reinterpret_cast<int64_t *>(sm + L::KV_SUM)))
+    if (!find_seq(a, false, 128, blockIdx.x / a.heads_kv, st))
         return;  // (an exit counts as both of the calls below)
     const int Lq = st->Lq, Lk = st->Lk, off = Lk - Lq, G = a.group;
     const int j0 = st->tile * 128;  // first key
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     // this launch leaves idle (they read nothing that it writes)
     wait_for_prerequisites();
     allow_dependents();
+    const bool bad = *reinterpret_cast<volatile int *>(a.status + 2) != 0;  // (read for the stores at the end)
 
     if (warp == 0) {
         // ---------------- producer: V once, then the query stages ----------------
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         if (ok && nt > 0) ok = wait_bar(done, 0, abort_flag, a.status, a.limit);
         tc_fence_after();
         // warp-uniform flags around the collective TMEM loads
-        const bool aborted = __any_sync(0xffffffffu, *abort_flag != 0);
+        const bool aborted = __any_sync(0xffffffffu, bad || *abort_flag != 0);
         const bool live = __all_sync(0xffffffffu, ok) && nt > 0;
         if (!aborted) {
             // warpgroup 0 writes the dV row, warpgroup 1 the dK row
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         tmem_alloc(reinterpret_cast<uint32_t *>(&sInt[0]), 512);
         tmem_relinquish();
     }
-    const bool good = borders_ok(a);
+    const bool good = borders_ok(a, threadIdx.x, kDqThreads);
     tc_fence_before();
     const bool go = !__syncthreads_or(!good);
     tc_fence_after();
@@ -936,7 +938,7 @@ static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_til
                                      cudaStream_t stream) {
     using namespace nabla::packed;
     cudaError_t err;
-    if (a.total_q > 0) {
+    {  // (without queries too: it looks at the borders)
         // heads a CTA of pre_kernel: 2 take 24 us at 100 MB, 1 27, 8 38; one where two
         // would not fill the GPU (six CTAs an SM)
         const int per = q_tiles * a.heads > 2 * 6 * kSms ? 2 : 1;
@@ -958,13 +960,8 @@ static cudaError_t launch_packed_bwd(const nabla::packed::Args &a, int64_t q_til
         constexpr uint32_t kSmem = KvLayout<D>::kSmem;
         err = nabla_allow_smem<dkdv_kernel<D>>(kSmem);
         if (err != cudaSuccess) return err;
-        const unsigned grid = static_cast<unsigned>(key_tiles * a.heads_kv);
-        if (q) {
-            err = nabla_launch_early(dkdv_kernel<D>, grid, kKvThreads, kSmem, stream, mq, mv128, mdo, a);
-        } else {  // without pre_kernel its predecessor is what clears the status, which it reads at once
-            dkdv_kernel<D><<<grid, kKvThreads, kSmem, stream>>>(mq, mv128, mdo, a);
-            err = cudaGetLastError();
-        }
+        err = nabla_launch_early(dkdv_kernel<D>, static_cast<unsigned>(key_tiles * a.heads_kv), kKvThreads, kSmem,
+                                 stream, mq, mv128, mdo, a);
         if (err != cudaSuccess) return err;
     }
     if (q) {

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tmem_relinquish();
     }
     // every CTA looks at every border before anything is written
-    const bool good = borders_ok(a) && (sb & 1023u) == 0;  // (swizzled tiles need the alignment asked for above)
+    const bool good = borders_ok(a, threadIdx.x, kFwdThreads) && (sb & 1023u) == 0;  // (swizzled tiles need the alignment asked for above)
     tc_fence_before();
     const bool go = !__syncthreads_or(!good);
     tc_fence_after();
