@@ -61,3 +61,28 @@ def test_many_sequences_one_bad_border(seqs):
     cu[seqs] += 1  # one row more than there are
     nabla.cache_append(k, v, kc, vc, table, starts, cu=cu.cuda(), ws=ws)
     assert nabla.status(ws) == nabla.ERR_PARAM and torch.equal(kc, before)
+
+
+@pytest.mark.parametrize("seqs,longest", [(1024, 40), (1025, 40), (3000, 12), (20000, 3)])
+def test_many_sequences(seqs, longest):
+    """Groups of rows that follow one another in a CTA, empty sequences among them."""
+    g = torch.Generator().manual_seed(seqs)
+    lens = torch.randint(0, longest + 1, (seqs,), generator=g)
+    lens[-1] = longest
+    starts = torch.randint(0, 9, (seqs,), generator=g)
+    cu = torch.cat([torch.zeros(1, dtype=torch.long), lens.cumsum(0)])
+    total, width = int(cu[-1]), -(-(longest + 9) // 16)
+    k, v, kc, vc, table = make(seqs, total + 3, width=width, heads_kv=1)
+    want = kc.clone(), vc.clone()
+    seq = torch.repeat_interleave(torch.arange(seqs), lens)
+    p = (starts[seq] + torch.arange(total) - cu[seq]).cuda()
+    at = table[seq.cuda(), p // 16].long(), p % 16
+    want[0][at], want[1][at] = k[:total], v[:total]
+    ws = nabla.cache_workspace("cuda")
+    nabla.cache_append(k, v, kc, vc, table, starts.to("cuda", torch.int32), cu=cu.to("cuda", torch.int32), ws=ws)
+    assert nabla.status(ws) == nabla.OK
+    assert torch.equal(kc, want[0]) and torch.equal(vc, want[1])
+    # a bad page under a late group of rows
+    table[int(seq[-2]), :] = -1
+    nabla.cache_append(k, v, kc, vc, table, starts.to("cuda", torch.int32), cu=cu.to("cuda", torch.int32), ws=ws)
+    assert nabla.status(ws) == nabla.ERR_PARAM
