@@ -503,116 +503,141 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const __grid_constan
     if (threadIdx.x == 0) a.flags[blockIdx.x] = any_bad;
 }
 
-// One CTA per (sequence, query head): adds the pieces of the CTAs that shared
-// it, in order, its NW warps taking every NW-th piece; writes empty rows; the
-// first CTA gathers the flags into the status word.
-template <int D, int NW>
+// One CTA per (sequence, query head), or with kRange one for a run of them: adds the
+// pieces of the CTAs that shared it, in order, its NW warps taking every NW-th
+// piece; writes empty rows; the first CTA gathers the flags into the status word.
+template <int D, int NW, bool kRange>
 __global__ void __launch_bounds__(32 * NW) join_kernel(const __grid_constant__ PagedArgs a) {
     constexpr int kPer = D / 32, NT = 32 * NW;
     __shared__ int64_t sums[2 * NW];
     __shared__ float so[NW][D], sw[kPagedCtas], part[2][NW];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
+    const int64_t rows = static_cast<int64_t>(a.c.seqs) * a.heads;
+    const int64_t row0 = kRange ? rows * blockIdx.x / gridDim.x : blockIdx.x;
+    int s = static_cast<int>(row0 / a.heads), head = static_cast<int>(row0 % a.heads);
     int64_t front, tiles;
     tile_sums<NT>(a, s, sums, &front, &tiles);
     bool bad = false;
-    const int nt = tiles_of(clean_len(a, s, &bad));
+    int nt = tiles_of(clean_len(a, s, &bad));
     const int per_seq = a.c.heads_kv * a.chunks;
-    const int hk = head / a.group, g = head % a.group;
-    const int pair = hk * a.chunks + g / kPagedHeads, r = g % kPagedHeads;
-    const int64_t W = tiles * per_seq, first = front * per_seq + static_cast<int64_t>(pair) * nt;
+    const int64_t W = tiles * per_seq;
     const int n = sharers(W, a.ctas);
-    // the CTA of unit u is the last one whose share begins at or before it
-    int c0 = 0, c1 = 0;
-    if (nt > 0) {
-        c0 = static_cast<int>(((first + 1) * n - 1) / W);
-        c1 = static_cast<int>(((first + nt) * n - 1) / W);
-    }
-    wait_for_prerequisites();
-    if (blockIdx.x == 0) {
-        for (int i = threadIdx.x; i < a.c.seqs; i += NT) clean_len(a, i, &bad);
-        for (int i = threadIdx.x; i < a.ctas; i += NT) bad |= a.flags[i] != 0;
-        bad = __syncthreads_or(bad);
-        if (threadIdx.x == 0) *a.status = bad ? kDevParam : kDevOk;
-    }
-    __nv_bfloat16 *dst = a.o + s * a.o_token + head * a.o_head;
-    float *lse = a.lse == nullptr ? nullptr : a.lse + static_cast<int64_t>(s) * a.heads + head;
-    if (nt == 0) {
-        for (int d = threadIdx.x; d < D; d += NT) dst[d] = __float2bfloat16_rn(0.f);
-        if (threadIdx.x == 0 && lse != nullptr) *lse = -INFINITY;
-        return;
-    }
-    if (c0 == c1) return;  // written whole
-    const int pieces = c1 - c0 + 1;
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(2 * a.ctas) * kPagedHeads * D);
-    // piece p: the first one began in its CTA (slot 1), the others in an earlier one (slot 0)
-    auto slot_of = [&](int p) { return static_cast<int64_t>(2 * (c0 + p) + (p == 0 ? 1 : 0)) * kPagedHeads + r; };
-    float m[(kPagedCtas + NT - 1) / NT], l[(kPagedCtas + NT - 1) / NT], M = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < (kPagedCtas + NT - 1) / NT; ++i) {
-        const int p = i * NT + threadIdx.x;
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        if (p < pieces) {
-            const float2 v = ml[slot_of(p)];
-            m[i] = v.x;
-            l[i] = v.y;
+    auto wait = [&]() {
+        wait_for_prerequisites();
+        if (blockIdx.x == 0) {
+            for (int i = threadIdx.x; i < a.c.seqs; i += NT) clean_len(a, i, &bad);
+            for (int i = threadIdx.x; i < a.ctas; i += NT) bad |= a.flags[i] != 0;
+            bad = __syncthreads_or(bad);
+            if (threadIdx.x == 0) *a.status = bad ? kDevParam : kDevOk;
         }
-        M = fmaxf(M, m[i]);
-    }
+    };
+    auto join = [&]() {
+        const int hk = head / a.group, g = head % a.group;
+        const int pair = hk * a.chunks + g / kPagedHeads, r = g % kPagedHeads;
+        const int64_t first = front * per_seq + static_cast<int64_t>(pair) * nt;
+        // the CTA of unit u is the last one whose share begins at or before it
+        int c0 = 0, c1 = 0;
+        if (nt > 0) {
+            c0 = static_cast<int>(((first + 1) * n - 1) / W);
+            c1 = static_cast<int>(((first + nt) * n - 1) / W);
+        }
+        if constexpr (!kRange) wait();
+        __nv_bfloat16 *dst = a.o + s * a.o_token + head * a.o_head;
+        float *lse = a.lse == nullptr ? nullptr : a.lse + static_cast<int64_t>(s) * a.heads + head;
+        if (nt == 0) {
+            for (int d = threadIdx.x; d < D; d += NT) dst[d] = __float2bfloat16_rn(0.f);
+            if (threadIdx.x == 0 && lse != nullptr) *lse = -INFINITY;
+            return;
+        }
+        if (c0 == c1) return;  // written whole
+        const int pieces = c1 - c0 + 1;
+        const float2 *ml = reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(2 * a.ctas) * kPagedHeads * D);
+        // piece p: the first one began in its CTA (slot 1), the others in an earlier one (slot 0)
+        auto slot_of = [&](int p) { return static_cast<int64_t>(2 * (c0 + p) + (p == 0 ? 1 : 0)) * kPagedHeads + r; };
+        float m[(kPagedCtas + NT - 1) / NT], l[(kPagedCtas + NT - 1) / NT], M = -INFINITY;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) part[0][warp] = M;
-    __syncthreads();
+        for (int i = 0; i < (kPagedCtas + NT - 1) / NT; ++i) {
+            const int p = i * NT + threadIdx.x;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            if (p < pieces) {
+                const float2 v = ml[slot_of(p)];
+                m[i] = v.x;
+                l[i] = v.y;
+            }
+            M = fmaxf(M, m[i]);
+        }
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, part[0][w]);
-    const float R = M == -INFINITY ? 0.f : M;
-    float total = 0.f;
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (lane == 0) part[0][warp] = M;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < (kPagedCtas + NT - 1) / NT; ++i) {
-        const int p = i * NT + threadIdx.x;
-        const float w = fast_exp2(m[i] - R);
-        if (p < pieces) sw[p] = w;
-        total += w * l[i];
-    }
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, part[0][w]);
+        const float R = M == -INFINITY ? 0.f : M;
+        float total = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) part[1][warp] = total;
-    __syncthreads();
-    total = 0.f;
+        for (int i = 0; i < (kPagedCtas + NT - 1) / NT; ++i) {
+            const int p = i * NT + threadIdx.x;
+            const float w = fast_exp2(m[i] - R);
+            if (p < pieces) sw[p] = w;
+            total += w * l[i];
+        }
 #pragma unroll
-    for (int w = 0; w < NW; ++w) total += part[1][w];
-    float o[kPer];
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (lane == 0) part[1][warp] = total;
+        __syncthreads();
+        total = 0.f;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+        for (int w = 0; w < NW; ++w) total += part[1][w];
+        float o[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] = 0.f;
 #pragma unroll 8
-    for (int p = warp; p < pieces; p += NW) {
-        const float *src = a.part + slot_of(p) * D + lane * kPer;
-        const float w = sw[p];
-        if constexpr (kPer == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(src);
-            o[0] += w * v.x;
-            o[1] += w * v.y;
-            o[2] += w * v.z;
-            o[3] += w * v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(src);
-            o[0] += w * v.x;
-            o[1] += w * v.y;
+        for (int p = warp; p < pieces; p += NW) {
+            const float *src = a.part + slot_of(p) * D + lane * kPer;
+            const float w = sw[p];
+            if constexpr (kPer == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(src);
+                o[0] += w * v.x;
+                o[1] += w * v.y;
+                o[2] += w * v.z;
+                o[3] += w * v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(src);
+                o[0] += w * v.x;
+                o[1] += w * v.y;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = o[e];
+        __syncthreads();
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        for (int d = threadIdx.x; d < D; d += NT) {
+            float x = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) x += so[w][d];
+            dst[d] = __float2bfloat16_rn(x * inv);
+        }
+        if (threadIdx.x == 0 && lse != nullptr)
+            *lse = total > 0.f ? (M + log2f(total)) * kLn2 : total == 0.f ? -INFINITY : total;
+    };
+    if constexpr (!kRange) {
+        join();
+    } else {
+        wait();
+        const int64_t count = rows * (blockIdx.x + 1) / gridDim.x - row0;
+        for (int64_t i = 0; i < count; ++i) {
+            if (i > 0) {
+                __syncthreads();  // the row before has been read from shared memory
+                if (++head == a.heads) {
+                    head = 0;
+                    front += nt;
+                    nt = tiles_of(clean_len(a, ++s, &bad));
+                }
+            }
+            join();
         }
     }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = o[e];
-    __syncthreads();
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    for (int d = threadIdx.x; d < D; d += NT) {
-        float x = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) x += so[w][d];
-        dst[d] = __float2bfloat16_rn(x * inv);
-    }
-    if (threadIdx.x == 0 && lse != nullptr)
-        *lse = total > 0.f ? (M + log2f(total)) * kLn2 : total == 0.f ? -INFINITY : total;
 }
 
 }  // namespace paged
@@ -637,6 +662,9 @@ cudaError_t nabla_launch_append(const nabla::AppendArgs &a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
+constexpr int kFewSeqs = 256;
+constexpr unsigned kJoinCtas = 16 * 148;  // of 128 threads, what runs at once
+
 template <int D>
 static cudaError_t launch_paged(const nabla::PagedArgs &a, cudaStream_t stream) {
     using namespace nabla::paged;
@@ -648,9 +676,15 @@ static cudaError_t launch_paged(const nabla::PagedArgs &a, cudaStream_t stream) 
     // few rows to join may each have hundreds of pieces: 16 warps a row (100,000
     // keys, 8 heads on one key head: 22 us against 37 with 4); many rows have a few
     // pieces each, which four warps add while other rows have theirs
+    // Every CTA looks at all lengths: with many sequences no more CTAs than run at once, or
+    // that work grows with their square (the whole call, up to 1,000 rows and 40 heads each:
+    // 256 sequences 152 us against 150 with a CTA a row, 512 254 against 260, 1,000 451 against
+    // 481; 6,000 of 20 rows and 8 heads 229 against 424)
     const unsigned rows = static_cast<unsigned>(a.c.seqs * a.heads);
-    return rows <= 148 ? nabla_launch_early(join_kernel<D, 16>, rows, 512, 0, stream, a)
-                       : nabla_launch_early(join_kernel<D, 4>, rows, 128, 0, stream, a);
+    if (rows <= 148) return nabla_launch_early(join_kernel<D, 16, false>, rows, 512, 0, stream, a);
+    if (a.c.seqs <= kFewSeqs || rows <= kJoinCtas)
+        return nabla_launch_early(join_kernel<D, 4, false>, rows, 128, 0, stream, a);
+    return nabla_launch_early(join_kernel<D, 4, true>, kJoinCtas, 128, 0, stream, a);
 }
 
 cudaError_t nabla_launch_paged(const nabla::PagedArgs &a, cudaStream_t stream) {
