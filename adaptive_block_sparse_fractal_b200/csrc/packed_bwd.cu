@@ -17,7 +17,7 @@
 //
 // Seven products per pair against the five that one kernel with atomic sums of
 // dQ would need: the price of sums whose order does not change.  P and dS are
-// rounded to bf16 for their MMAs (2^-9 relative each), everything else is
+// rounded to bf16 for their MMAs (by up to 2^-8 relative each), everything else is
 // float32.  MMAs go out four per elect.sync from converged warps (an N = 64 MMA
 // is accepted about when it starts, so the issuer must not fall behind).
 //

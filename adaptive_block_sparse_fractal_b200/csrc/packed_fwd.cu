@@ -19,8 +19,8 @@
 // exponentials the SFU another 1,024 (16 a cycle and SM), so part of them is
 // taken on the FMA pipe instead: 2^x = 2^n p(x - n), n the nearest integer, p
 // the degree-4 polynomial that minimises the largest relative error of 2^f on
-// [-1/2, 1/2] (2.6e-6, found with a Remez iteration; P is rounded to bf16, at
-// 2e-3, next).
+// [-1/2, 1/2] (2.6e-6, found with a Remez iteration; P is rounded to bf16, by up to
+// 2^-8, next).
 //
 // A row's reference is the maximum of its first tile (and of masked ones).
 // Other tiles are taken against it without looking for their own maximum: P
@@ -73,9 +73,9 @@ constexpr int kRegsFew = 64, kRegsMany = 104;
 constexpr int kTileKeys = 128;
 constexpr float kFwdLn2 = 0.6931471805599453f;
 constexpr float kMaxSum = 1152921504606846976.f;  // 2^60: largest sum of P over a tile's half row
-// pairs of every 8 whose exponentials the FMA pipe takes.  D = 128, dense: 1 of 8
-// 1,332 TFLOP/s, 2 1,381, 3 1,332; D = 64, where the tensor core has half the
-// work and instruction issue is short: 0 739, 1 785, 2 760, 3 704.
+// pairs of every 8 whose exponentials the FMA pipe takes.  8,192 dense tokens, 40/8
+// heads, D = 128: 1 of 8 1,364 TFLOP/s, 2 1,372, 3 1,331; D = 64, where the tensor core
+// has half the work and instruction issue is short: 0 and 1 alike, 2 2% and 3 6% slower.
 template <int D>
 constexpr int kPolyOf8 = D == 128 ? 2 : 1;
 

@@ -6,8 +6,9 @@
 // every CTA looks at every border: if one does not ascend or leaves the rows given,
 // none writes anything.
 //
-// paged attention: every cached row is read once, 4 D bytes for 4 D flop and
-// query head, so HBM bounds it at any group size.  Work is cut into tiles of 64
+// paged attention: every cached row is read once for up to 16 query heads of its key
+// head, 4 D bytes for 4 D flop and query head, so HBM bounds it (a larger group is
+// cut into chunks of 16, each of which reads the rows again).  Work is cut into tiles of 64
 // keys of one (sequence, key head, chunk of up to 16 query heads); the tiles of
 // the whole batch form one line, which the CTAs share out evenly, so ragged
 // lengths and a single long sequence balance alike.  A CTA therefore owns a

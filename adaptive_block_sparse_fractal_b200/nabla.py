@@ -484,7 +484,7 @@ def attn_packed_fwd(q, k, v, cu_q, cu_k, causal=False, scale=None, o=None, lse=N
     heads_kv, D] (bf16, any strides of 16 bytes with contiguous rows), borders
     cu_q, cu_k int32 [seqs + 1].  causal aligns the last rows of q and k.
     Returns o (laid out like q) and lse float32 [heads, total_q]; rows of no
-    sequence are left as they were."""
+    sequence are left as they were, and hold anything where o is not given."""
     dev = _device(q, "q")
     bf = torch.bfloat16
     shape = _packed_of(q, k, cu_q, causal, scale)
@@ -503,7 +503,8 @@ def attn_packed_fwd(q, k, v, cu_q, cu_k, causal=False, scale=None, o=None, lse=N
 
 def attn_packed_bwd(q, k, v, o, dout, lse, cu_q, cu_k, causal=False, scale=None, dq=None, dk=None,
                     dv=None, ws=None):
-    """Gradients dq, dk, dv of attn_packed_fwd from its o and lse."""
+    """Gradients dq, dk, dv of attn_packed_fwd from its o and lse; rows of no
+    sequence as there."""
     dev = _device(q, "q")
     bf = torch.bfloat16
     shape = _packed_of(q, k, cu_q, causal, scale)

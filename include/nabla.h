@@ -357,11 +357,12 @@ int nabla_rope(const nabla_rope_params *params, int B, int T, int H, int W, int 
  * cu_q[s] .. cu_q[s+1]-1 of q and cu_k[s] .. cu_k[s+1]-1 of k, v (int32
  * [seqs + 1] each, ascending from >= 0; the two may be one array).  heads is a
  * multiple of heads_kv: query head h reads key head h / (heads / heads_kv).
- *   causal  row i of Lq keeps the keys j <= i + Lk - Lq of its sequence (the
- *           last rows of both coincide); otherwise it keeps all of them.
+ *   causal  1: row i of Lq keeps the keys j <= i + Lk - Lq of its sequence (the
+ *           last rows of both coincide); 0: it keeps all of them.  (The test aid
+ *           NABLA_DEBUG_TIMEOUT may be or-ed into it.)
  * Rows of q and k that belong to no sequence are neither read into a result nor
- * written.  D in {64, 128}, at most 65535 heads, 128 of them a key head; pointers and
- * distances multiples of 16 bytes.
+ * written.  D in {64, 128}, at most 65535 heads, 128 of them a key head, and 2^24
+ * sequences; pointers and distances multiples of 16 bytes, distances above 0.
  * Borders that do not ascend, or that leave [0, total], make the call write
  * NABLA_ERR_PARAM to the workspace status and leave the outputs unwritten.
  * NaN and infinities in rows of other sequences, or of none, never reach a
