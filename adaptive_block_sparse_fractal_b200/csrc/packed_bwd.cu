@@ -141,8 +141,12 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     volatile int *abort_flag = sInt + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hk = static_cast<int>(blockIdx.x % a.heads_kv);
-    if (!find_seq(a, false, 128, blockIdx.x / a.heads_kv, st))
-        return;  // (an exit counts as both of the calls below)
+    if (!find_seq(a, false, 128, blockIdx.x / a.heads_kv, st)) {
+        // (an exit counts as both of the calls below; behind the wait, so that dQ, and with it
+        // the end of the call, never comes in front of the end of pre_kernel)
+        wait_for_prerequisites();
+        return;
+    }
     const int Lq = st->Lq, Lk = st->Lk, off = Lk - Lq, G = a.group;
     const int j0 = st->tile * 128;  // first key
     // query tiles [qs, qs + per) of each head: query i keeps keys up to i + off
